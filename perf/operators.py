@@ -185,7 +185,7 @@ def _act(g, act):
     if act == "silu":
         return g * _sigmoid(g)
     if act == "gelu":
-        return 0.5 * g * (1 + torch.erf(g * math.sqrt(0.5)))
+        return 0.5 * g * torch.erfc(-g * math.sqrt(0.5))   # no cancellation for g < 0
     if act == "gelu_tanh":   # 0.5 (1 + tanh z) = sigmoid(2 z)
         return g * _sigmoid(2 * math.sqrt(2 / math.pi) * (g + 0.044715 * g * g * g))
     return torch.where(g > 0, g, torch.zeros_like(g))
@@ -196,7 +196,7 @@ def _act_slope(g, act):
         s = _sigmoid(g)
         return s * (1 + g * (1 - s))
     if act == "gelu":
-        return (0.5 * (1 + torch.erf(g * math.sqrt(0.5)))
+        return (0.5 * torch.erfc(-g * math.sqrt(0.5))
                 + g * torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi))
     if act == "gelu_tanh":
         c = math.sqrt(2 / math.pi)
@@ -322,7 +322,7 @@ def _exact_act(g, act):
         s = torch.special.expit(g)
         return g * s, s + g * s * torch.special.expit(-g)
     if act == "gelu":
-        phi = torch.special.ndtr(g)
+        phi = torch.special.erfc(-g * math.sqrt(0.5)) / 2
         return g * phi, phi + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
     if act == "gelu_tanh":
         c = math.sqrt(2 / math.pi)
