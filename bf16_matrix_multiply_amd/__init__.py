@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import typing
 
 import torch
 
@@ -27,7 +28,8 @@ __all__ = ["BmmError", "pack_operand", "pack_operand_kmajor", "box_copy", "box_s
            "box_reduce_add", "mma_tile", "mma_tile_splitk", "mma_tile_splitk_noalloc",
            "splitk_default", "splitk_suggested", "NOALLOC_SCRATCH_BYTES",
            "splitk_workspace_bytes", "select_kernel", "library_path", "KERNELS", "MmaOpts",
-           "ELEM_TYPES"]
+           "ELEM_TYPES", "ACTS", "gated", "gated_backward", "gated_backward_workspace_bytes",
+           "Mx4Operand", "mx4_quantize", "mx4_dequantize", "mx4_mma", "mx4_gated"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbmm.so")
@@ -38,6 +40,9 @@ _DTYPES = {"f16": BMM_F16, "float16": BMM_F16, torch.float16: BMM_F16,
 KERNELS = {"auto": 0, "direct": 1, "tiled": 2, "skinny": 3, "tiled128": 4, "tiled256x128": 5}
 NOALLOC_SCRATCH_BYTES = 64 << 20   # BMM_NOALLOC_SCRATCH_BYTES
 ELEM_TYPES = {"f32": 1, "f16": 2, "bf16": 3, "i32": 4, "i64": 5}
+ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+_HALF_DTYPES = {torch.float16: BMM_F16, torch.bfloat16: BMM_BF16}
+_ELEM_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
 
@@ -69,6 +74,19 @@ class MmaOpts(ctypes.Structure):
         ("scaled", ctypes.c_int32),
         ("alpha", ctypes.c_float),
         ("beta", ctypes.c_float),
+    ]
+
+
+class GatedDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("M", ctypes.c_int64),
+        ("F", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_h", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
     ]
 
 
@@ -122,6 +140,21 @@ def lib():
                   L.bmm_mma_tile_opts, L.bmm_select_kernel, L.bmm_box_store,
                   L.bmm_box_reduce_add, L.bmm_mma_tile_splitk, L.bmm_mma_tile_splitk_noalloc,
                   L.bmm_splitk_default, L.bmm_splitk_suggested):
+            f.restype = ctypes.c_int
+        desc = ctypes.POINTER(GatedDesc)
+        L.bmm_gated.argtypes = [p] * 6 + [desc, p]
+        L.bmm_gated_backward.argtypes = [p] * 9 + [desc, p, i64, p]
+        L.bmm_gated_backward_workspace_bytes.argtypes = [desc]
+        L.bmm_gated_backward_workspace_bytes.restype = i64
+        for f in (L.bmm_mx4_codes_bytes, L.bmm_mx4_scales_bytes):
+            f.argtypes = [i64, i64, i64]
+            f.restype = i64
+        L.bmm_mx4_quantize.argtypes = [p, p, p, i64, i64, i64, i64, i32, p]
+        L.bmm_mx4_dequantize.argtypes = [p, p, p, i64, i64, i64, i64, i32, p]
+        L.bmm_mx4_mma.argtypes = [p] * 5 + [i64] * 5 + [i32, p]
+        L.bmm_mx4_gated.argtypes = [p] * 7 + [i64] * 5 + [i32, i32, p]
+        for f in (L.bmm_gated, L.bmm_gated_backward, L.bmm_mx4_quantize, L.bmm_mx4_dequantize,
+                  L.bmm_mx4_mma, L.bmm_mx4_gated):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -438,3 +471,247 @@ def mma_tile(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None,
 
 def select_kernel(batch: int, M_rep: int, N_rep: int, K_rep: int) -> str:
     return KERNEL_NAMES[_check(lib().bmm_select_kernel(batch, M_rep, N_rep, K_rep))]
+
+
+# ---- feed-forward operators ----
+
+def _act_code(act: str, fn: str) -> int:
+    try:
+        return ACTS[act]
+    except (KeyError, TypeError):
+        raise ValueError(f"{fn}: unknown activation {act!r}; expected one of {sorted(ACTS)}") from None
+
+
+def _rows_ld(t: torch.Tensor, name: str, fn: str) -> int:
+    """Elements between the rows of a (rows, cols) or (batch, rows, cols) matrix
+    with unit innermost stride and batches rows * ld apart."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{fn}: {name} must be (rows, cols) or (batch, rows, cols)")
+    rows, cols = t.shape[-2:]
+    if t.numel() == 0:
+        return -(-cols // 8) * 8
+    ld = t.stride(-2) if rows > 1 else \
+        (t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else -(-cols // 8) * 8)
+    if (t.stride(-1) != 1 and cols > 1) or \
+            (t.dim() == 3 and t.shape[0] > 1 and t.stride(0) != rows * ld):
+        raise ValueError(f"{fn}: {name} must have unit innermost stride and dense batches")
+    return ld
+
+
+def _out(t, shape, dtype, device, name, fn):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _gated_weights(Wg, Wu, batch, K, fn) -> int:
+    """F of two packed weights (batch, F/8, K/16, 8, 8)."""
+    for w, name in ((Wg, "Wg"), (Wu, "Wu")):
+        if w.dim() != 5 or w.shape[3:] != (8, 8) or w.element_size() != 4 or not w.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous packed words (batch, F/8, K/16, 8, 8) "
+                             "(pack_operand with atom_rows 8)")
+    if Wg.shape != Wu.shape:
+        raise ValueError(f"{fn}: Wg and Wu differ in shape")
+    if Wg.shape[0] != batch or 16 * Wg.shape[2] != K:
+        raise ValueError(f"{fn}: X and the weights disagree on batch or K")
+    return 8 * Wg.shape[1]
+
+
+def _half_matrix(t, name, fn):
+    try:
+        return _HALF_DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"{fn}: {name} must be float16 or bfloat16, got {t.dtype}") from None
+
+
+def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu",
+          save: bool = False, out: torch.Tensor | None = None):
+    """H = act(X Wg^T) * (X Wu^T) (bmm_gated): the gated half of a feed-forward
+    block in one kernel.
+
+    X is (M, K) or (batch, M, K) float16 or bfloat16, rows any multiple of 8
+    elements apart; Wg and Wu are packed B operands (pack_operand(w, 8)) of
+    the same type. Returns H (..., M, F) in X's type, and with ``save`` (H, G,
+    U), the projections that gated_backward takes. ``act`` is one of ACTS."""
+    code = _act_code(act, "gated")
+    _require_cuda(X, Wg, Wu, out)
+    dt = _half_matrix(X, "X", "gated")
+    ld_x = _rows_ld(X, "X", "gated")
+    batch = X.shape[0] if X.dim() == 3 else 1
+    M, K = X.shape[-2:]
+    F = _gated_weights(Wg, Wu, batch, K, "gated")
+    shape = (*X.shape[:-1], F)
+    H = _out(out, shape, X.dtype, X.device, "out", "gated")
+    ld_h = _rows_ld(H, "out", "gated")
+    G = U = None
+    if save:
+        if ld_h != F and H.numel():
+            raise ValueError("gated: with save, out must be contiguous")
+        G, U = torch.empty_like(H), torch.empty_like(H)
+    d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
+    _check(lib().bmm_gated(_ptr(H), _ptr(G), _ptr(U), _ptr(X), _ptr(Wg), _ptr(Wu),
+                           ctypes.byref(d), _stream(X)))
+    return (H, G, U) if save else H
+
+
+def gated_backward_workspace_bytes(batch: int, M: int, F: int, K: int) -> int:
+    """bmm_gated_backward_workspace_bytes for these extents."""
+    d = GatedDesc(batch, M, F, K, K, F, BMM_BF16, 0)
+    return _check(lib().bmm_gated_backward_workspace_bytes(ctypes.byref(d)))
+
+
+def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.Tensor,
+                   Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", need_dx: bool = True,
+                   need_dw: bool = True, workspace: torch.Tensor | None = None):
+    """Gradients of gated (bmm_gated_backward): (dX, dWg, dWu) for dH = dL/dH and
+    the projections G and U that gated(..., save=True) returned.
+
+    dX is (..., M, K); dWg and dWu are row-major (F, K) ((batch, F, K) for a
+    batched X), all in X's type; None stands for what need_dx or need_dw leaves
+    out. dH, G and U share one row stride. ``workspace`` (any contiguous
+    tensor of at least gated_backward_workspace_bytes) is allocated here when
+    not given."""
+    fn = "gated_backward"
+    code = _act_code(act, fn)
+    if not (need_dx or need_dw):
+        raise ValueError(f"{fn}: neither need_dx nor need_dw")
+    _require_cuda(dH, G, U, X, Wg, Wu, workspace)
+    dt = _half_matrix(X, "X", fn)
+    ld_x = _rows_ld(X, "X", fn)
+    batch = X.shape[0] if X.dim() == 3 else 1
+    M, K = X.shape[-2:]
+    F = _gated_weights(Wg, Wu, batch, K, fn)
+    ld_h = _rows_ld(dH, "dH", fn)
+    for t, name in ((dH, "dH"), (G, "G"), (U, "U")):
+        if tuple(t.shape) != (*X.shape[:-1], F) or t.dtype != X.dtype:
+            raise ValueError(f"{fn}: {name} must be a {X.dtype} tensor of shape {(*X.shape[:-1], F)}")
+        if _rows_ld(t, name, fn) != ld_h:
+            raise ValueError(f"{fn}: dH, G and U must have the same row stride")
+    d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
+    need = _check(lib().bmm_gated_backward_workspace_bytes(ctypes.byref(d)))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device) if need_dx else None
+    dWg = dWu = None
+    if need_dw:
+        dWg = torch.empty((*X.shape[:-2], F, K), dtype=X.dtype, device=X.device)
+        dWu = torch.empty_like(dWg)
+    _check(lib().bmm_gated_backward(_ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(dH), _ptr(G), _ptr(U),
+                                    _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(d), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(X)))
+    return dX, dWg, dWu
+
+
+class Mx4Operand(typing.NamedTuple):
+    """A 4-bit operand: codes (batch, ceil(rows/16), ceil(K/128), 4, 16, 16) and
+    scales (batch, ceil(rows/16), ceil(K/512), 4, 16, 4) uint8, of a (rows, K)
+    matrix, or with ``batched`` a (batch, rows, K) one (include/bmm.h gives
+    the layout)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    rows: int
+    K: int
+    batched: bool = False
+
+    @property
+    def batch(self) -> int:
+        return self.codes.shape[0]
+
+
+def _mx4_shapes(batch, rows, K):
+    r16 = -(-rows // 16)
+    return (batch, r16, -(-K // 128), 4, 16, 16), (batch, r16, -(-K // 512), 4, 16, 4)
+
+
+def _mx4_check(op: Mx4Operand, name, fn):
+    want = _mx4_shapes(op.batch, op.rows, op.K)
+    for t, shape, part in ((op.codes, want[0], "codes"), (op.scales, want[1], "scales")):
+        if tuple(t.shape) != shape or t.dtype != torch.uint8 or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name}.{part} must be a contiguous uint8 tensor of shape {shape}")
+    if op.batch != 1 and not op.batched:
+        raise ValueError(f"{fn}: {name} has {op.batch} batches but is not batched")
+    _require_cuda(op.codes, op.scales)
+
+
+def mx4_quantize(X: torch.Tensor) -> Mx4Operand:
+    """(rows, K) or (batch, rows, K) float32, float16 or bfloat16 to a 4-bit
+    operand (bmm_mx4_quantize): blocks of 32 along K, one power-of-two scale
+    each. K is a multiple of 32; rows may be any multiple of 8 elements apart."""
+    _require_cuda(X)
+    if X.dtype not in _ELEM_DTYPES:
+        raise ValueError(f"mx4_quantize: X must be float32, float16 or bfloat16, got {X.dtype}")
+    ld = _rows_ld(X, "X", "mx4_quantize")
+    batch = X.shape[0] if X.dim() == 3 else 1
+    rows, K = X.shape[-2:]
+    cs, ss = _mx4_shapes(batch, rows, K)
+    codes = torch.empty(cs, dtype=torch.uint8, device=X.device)
+    scales = torch.empty(ss, dtype=torch.uint8, device=X.device)
+    _check(lib().bmm_mx4_quantize(_ptr(codes), _ptr(scales), _ptr(X), batch, rows, K, ld,
+                                  _ELEM_DTYPES[X.dtype], _stream(X)))
+    return Mx4Operand(codes, scales, rows, K, X.dim() == 3)
+
+
+def mx4_dequantize(A: Mx4Operand, dtype: torch.dtype = torch.float32,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """The (rows, K) or (batch, rows, K) values of a 4-bit operand in ``dtype``
+    (bmm_mx4_dequantize)."""
+    _mx4_check(A, "A", "mx4_dequantize")
+    _require_cuda(out)
+    if dtype not in _ELEM_DTYPES:
+        raise ValueError(f"mx4_dequantize: dtype must be float32, float16 or bfloat16, got {dtype}")
+    shape = (A.batch, A.rows, A.K) if A.batched else (A.rows, A.K)
+    out = _out(out, shape, dtype, A.codes.device, "out", "mx4_dequantize")
+    ld = _rows_ld(out, "out", "mx4_dequantize")
+    _check(lib().bmm_mx4_dequantize(_ptr(out), _ptr(A.codes), _ptr(A.scales), A.batch, A.rows, A.K,
+                                    ld, _ELEM_DTYPES[dtype], _stream(A.codes)))
+    return out
+
+
+def mx4_mma(A: Mx4Operand, B: Mx4Operand, dtype: torch.dtype = torch.float32,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """D = A * B^T over 4-bit operands (bmm_mx4_mma): row-major (M, N) or (batch,
+    M, N) in ``dtype`` (float32, float16 or bfloat16). B's rows are a multiple
+    of 8."""
+    _mx4_check(A, "A", "mx4_mma")
+    _mx4_check(B, "B", "mx4_mma")
+    _require_cuda(out)
+    if dtype not in _ELEM_DTYPES:
+        raise ValueError(f"mx4_mma: dtype must be float32, float16 or bfloat16, got {dtype}")
+    if A.batch != B.batch or A.K != B.K:
+        raise ValueError("mx4_mma: A and B disagree on batch or K")
+    shape = (A.batch, A.rows, B.rows) if A.batched else (A.rows, B.rows)
+    out = _out(out, shape, dtype, A.codes.device, "out", "mx4_mma")
+    ld = _rows_ld(out, "out", "mx4_mma")
+    _check(lib().bmm_mx4_mma(_ptr(out), _ptr(A.codes), _ptr(A.scales), _ptr(B.codes),
+                             _ptr(B.scales), A.batch, A.rows, B.rows, A.K, ld,
+                             _ELEM_DTYPES[dtype], _stream(A.codes)))
+    return out
+
+
+def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
+              dtype: torch.dtype = torch.bfloat16,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """H = act(X Wg^T) * (X Wu^T) over 4-bit operands (bmm_mx4_gated): row-major
+    (M, F) or (batch, M, F) in ``dtype`` (float16 or bfloat16). The weights' F
+    rows are a multiple of 8."""
+    code = _act_code(act, "mx4_gated")
+    for op, name in ((X, "X"), (Wg, "Wg"), (Wu, "Wu")):
+        _mx4_check(op, name, "mx4_gated")
+    _require_cuda(out)
+    if dtype not in _HALF_DTYPES:
+        raise ValueError(f"mx4_gated: dtype must be float16 or bfloat16, got {dtype}")
+    if Wg.rows != Wu.rows or Wg.K != Wu.K or Wg.batch != Wu.batch:
+        raise ValueError("mx4_gated: Wg and Wu differ in shape")
+    if X.batch != Wg.batch or X.K != Wg.K:
+        raise ValueError("mx4_gated: X and the weights disagree on batch or K")
+    shape = (X.batch, X.rows, Wg.rows) if X.batched else (X.rows, Wg.rows)
+    out = _out(out, shape, dtype, X.codes.device, "out", "mx4_gated")
+    ld = _rows_ld(out, "out", "mx4_gated")
+    _check(lib().bmm_mx4_gated(_ptr(out), _ptr(X.codes), _ptr(X.scales), _ptr(Wg.codes),
+                               _ptr(Wg.scales), _ptr(Wu.codes), _ptr(Wu.scales), X.batch, X.rows,
+                               Wg.rows, X.K, ld, code, _ELEM_DTYPES[dtype], _stream(X.codes)))
+    return out

@@ -1,0 +1,270 @@
+// extern "C" entry points of the feed-forward operators (include/bmm.h):
+// validate on the host, then enqueue the kernels on the caller's stream.
+#include <exception>
+#include <string>
+
+#include "ffn.h"
+#include "validate.h"
+
+namespace {
+
+int report(const bmm::Status& st) {
+  bmm::set_last_error(st.msg);
+  return st.code;
+}
+
+int hip_status(hipError_t e, const char* what) {
+  if (e == hipSuccess) return report(bmm::Status{});
+  bmm::set_last_error(std::string(what) + ": " + hipGetErrorString(e));
+  return BMM_EHIP;
+}
+
+// No exception (out of host memory in a message, say) leaves a C entry point.
+template <class Fn>
+auto guarded(Fn fn) noexcept -> decltype(fn()) {
+  try {
+    return fn();
+  } catch (...) {
+    return BMM_EHIP;
+  }
+}
+
+// Start of the second block of output rows where there is none.
+constexpr int64_t kNoRow = int64_t(1) << 62;
+
+int64_t padded_width(int64_t F) { return (F + 31) / 32 * 32; }
+
+// Layout of the backward pass's workspace: [dG | dU], then the partial sums of
+// one product at a time.
+struct BackwardPlan {
+  int64_t slopes_bytes, need;
+  int dx_splits, dw_splits;
+};
+
+BackwardPlan plan_backward(const bmm_gated_desc& d) {
+  BackwardPlan p;
+  const int64_t Fp2 = 2 * padded_width(d.F);
+  p.slopes_bytes = (d.batch * d.M * Fp2 * 2 + 255) / 256 * 256;
+  p.dx_splits = bmm::ffn_splits(d.batch, d.M, d.K, Fp2);
+  p.dw_splits = bmm::ffn_splits(d.batch, Fp2, d.K, d.M);
+  const int64_t dx = p.dx_splits > 1 ? p.dx_splits * d.batch * d.M * d.K * 4 : 0;
+  const int64_t dw = p.dw_splits > 1 ? p.dw_splits * d.batch * Fp2 * d.K * 4 : 0;
+  p.need = p.slopes_bytes + (dx > dw ? dx : dw);
+  return p;
+}
+
+bmm::TileArgs gated_args(const bmm_gated_desc& d) {
+  bmm::TileArgs a{};
+  a.batch = d.batch;
+  a.act = d.act;
+  a.out_type = d.dtype == BMM_BF16 ? BMM_ELEM_BF16 : BMM_ELEM_F16;
+  a.splits = 1;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const uint32_t* Wg,
+              const uint32_t* Wu, const bmm_gated_desc* desc, void* stream) {
+  return guarded([&] {
+    const bmm::Status st = bmm::check_gated(H, G, U, X, Wg, Wu, desc);
+    if (!st.ok()) return report(st);
+    const bmm_gated_desc& d = *desc;
+    if (d.batch == 0 || d.M == 0 || d.F == 0) return report(st);
+    bmm::TileArgs a = gated_args(d);
+    a.a = X;
+    a.b0 = Wg;
+    a.b1 = Wu;
+    a.d = H;
+    a.d1 = G;
+    a.d2 = U;
+    a.M = d.M;
+    a.N = d.F;
+    a.K = d.K;
+    a.lda = d.ld_x;
+    a.ldd = d.ld_h;
+    a.a_bs = d.M * d.ld_x;
+    a.b_bs = d.F * d.K;
+    return hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
+                      "gated launch");
+  });
+}
+
+int64_t bmm_gated_backward_workspace_bytes(const bmm_gated_desc* desc) {
+  return guarded([&]() -> int64_t {
+    const bmm::Status st = bmm::check_gated_desc(desc, "gated_backward");
+    if (!st.ok()) return report(st);
+    return plan_backward(*desc).need;
+  });
+}
+
+int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_t* dH,
+                       const uint16_t* G, const uint16_t* U, const uint16_t* X,
+                       const uint32_t* Wg, const uint32_t* Wu, const bmm_gated_desc* desc,
+                       void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    bmm::Status st = bmm::check_gated_desc(desc, "gated_backward");
+    if (!st.ok()) return report(st);
+    const bmm_gated_desc& d = *desc;
+    const BackwardPlan plan = plan_backward(d);
+    st = bmm::check_gated_backward(dX, dWg, dWu, dH, G, U, X, Wg, Wu, desc, workspace,
+                                   workspace_bytes, plan.need);
+    if (!st.ok()) return report(st);
+    if (d.batch == 0 || d.K == 0 || (d.M == 0 && d.F == 0)) return report(st);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    uint16_t* const dgu = static_cast<uint16_t*>(workspace);
+    float* const part =
+        reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.slopes_bytes);
+    const int64_t Fp = padded_width(d.F);
+    int rc = hip_status(bmm::launch_gated_slopes(dgu, dH, G, U, d.batch * d.M, d.F, d.ld_h,
+                                                 d.dtype, d.act, s),
+                        "gated_backward slopes launch");
+    if (rc != BMM_OK) return rc;
+    if (dX && d.M > 0) {
+      bmm::TileArgs a = gated_args(d);
+      a.a = dgu;
+      a.b0 = Wg;
+      a.b1 = Wu;
+      a.d = dX;
+      a.M = a.rows0 = d.M;
+      a.row1 = kNoRow;
+      a.N = a.ldd = d.K;
+      a.K = a.lda = 2 * Fp;
+      a.a_bs = d.M * 2 * Fp;
+      a.b_bs = d.F * d.K;
+      a.b_sum = Fp;
+      a.b_rows = d.F;
+      a.splits = plan.dx_splits;
+      a.part = part;
+      a.part_floats = d.batch * d.M * d.K;
+      rc = hip_status(bmm::launch_gated_dx(a, d.dtype, s), "gated_backward dX launch");
+      if (rc != BMM_OK) return rc;
+    }
+    if (dWg && d.F > 0) {
+      bmm::TileArgs a = gated_args(d);
+      a.a = dgu;
+      a.b0 = X;
+      a.d = dWg;
+      a.d1 = dWu;
+      a.M = a.lda = 2 * Fp;
+      a.rows0 = d.F;
+      a.row1 = Fp;
+      a.N = a.ldd = d.K;
+      a.K = d.M;
+      a.ldb = d.ld_x;
+      a.a_bs = d.M * 2 * Fp;
+      a.b_bs = d.M * d.ld_x;
+      a.splits = plan.dw_splits;
+      a.part = part;
+      a.part_floats = d.batch * 2 * Fp * d.K;
+      rc = hip_status(bmm::launch_gated_dw(a, d.dtype, s), "gated_backward dW launch");
+    }
+    return rc;
+  });
+}
+
+int64_t bmm_mx4_codes_bytes(int64_t batch, int64_t rows, int64_t K) {
+  const int64_t n = bmm::mx4_codes_bytes(batch, rows, K);
+  return n < 0 ? BMM_EINVAL : n;
+}
+
+int64_t bmm_mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K) {
+  const int64_t n = bmm::mx4_scales_bytes(batch, rows, K);
+  return n < 0 ? BMM_EINVAL : n;
+}
+
+int bmm_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t batch, int64_t rows,
+                     int64_t K, int64_t ld_src, int32_t elem_type, void* stream) {
+  return guarded([&] {
+    const bmm::Status st = bmm::check_mx4_convert(src, codes, scales, batch, rows, K, ld_src,
+                                                  elem_type, "mx4_quantize");
+    if (!st.ok()) return report(st);
+    if (batch == 0 || rows == 0 || K == 0) return report(st);
+    return hip_status(bmm::launch_mx4_quantize(codes, scales, src, batch, rows, K, ld_src,
+                                               elem_type, static_cast<hipStream_t>(stream)),
+                      "mx4_quantize launch");
+  });
+}
+
+int bmm_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales, int64_t batch,
+                       int64_t rows, int64_t K, int64_t ld_dst, int32_t elem_type, void* stream) {
+  return guarded([&] {
+    const bmm::Status st = bmm::check_mx4_convert(dst, codes, scales, batch, rows, K, ld_dst,
+                                                  elem_type, "mx4_dequantize");
+    if (!st.ok()) return report(st);
+    if (batch == 0 || rows == 0 || K == 0) return report(st);
+    return hip_status(bmm::launch_mx4_dequantize(dst, codes, scales, batch, rows, K, ld_dst,
+                                                 elem_type, static_cast<hipStream_t>(stream)),
+                      "mx4_dequantize launch");
+  });
+}
+
+int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* B_codes,
+                const uint8_t* B_scales, int64_t batch, int64_t M, int64_t N, int64_t K,
+                int64_t ld_d, int32_t elem_type, void* stream) {
+  return guarded([&] {
+    const bmm::Status st =
+        bmm::check_mx4_product(D, A_codes, A_scales, B_codes, B_scales, nullptr, nullptr, false,
+                               batch, M, N, K, ld_d, 0, elem_type);
+    if (!st.ok()) return report(st);
+    if (batch == 0 || M == 0 || N == 0) return report(st);
+    bmm::TileArgs a{};
+    a.a = A_codes;
+    a.as = A_scales;
+    a.b0 = B_codes;
+    a.bs0 = B_scales;
+    a.d = D;
+    a.batch = batch;
+    a.M = a.rows0 = M;
+    a.row1 = kNoRow;
+    a.N = N;
+    a.K = K;
+    a.ldd = ld_d;
+    a.a_bs = bmm::mx4_codes_bytes(1, M, K);
+    a.as_bs = bmm::mx4_scales_bytes(1, M, K);
+    a.b_bs = bmm::mx4_codes_bytes(1, N, K);
+    a.bs_bs = bmm::mx4_scales_bytes(1, N, K);
+    a.out_type = elem_type;
+    a.splits = 1;
+    return hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
+  });
+}
+
+int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
+                  const uint8_t* Wg_codes, const uint8_t* Wg_scales, const uint8_t* Wu_codes,
+                  const uint8_t* Wu_scales, int64_t batch, int64_t M, int64_t F, int64_t K,
+                  int64_t ld_h, int32_t act, int32_t elem_type, void* stream) {
+  return guarded([&] {
+    const bmm::Status st =
+        bmm::check_mx4_product(H, X_codes, X_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
+                               true, batch, M, F, K, ld_h, act, elem_type);
+    if (!st.ok()) return report(st);
+    if (batch == 0 || M == 0 || F == 0) return report(st);
+    bmm::TileArgs a{};
+    a.a = X_codes;
+    a.as = X_scales;
+    a.b0 = Wg_codes;
+    a.bs0 = Wg_scales;
+    a.b1 = Wu_codes;
+    a.bs1 = Wu_scales;
+    a.d = H;
+    a.batch = batch;
+    a.M = M;
+    a.N = F;
+    a.K = K;
+    a.ldd = ld_h;
+    a.a_bs = bmm::mx4_codes_bytes(1, M, K);
+    a.as_bs = bmm::mx4_scales_bytes(1, M, K);
+    a.b_bs = bmm::mx4_codes_bytes(1, F, K);
+    a.bs_bs = bmm::mx4_scales_bytes(1, F, K);
+    a.act = act;
+    a.out_type = elem_type;
+    a.splits = 1;
+    return hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
+                      "mx4_gated launch");
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,150 @@
+// The backward pass of H = act(G) * U, G = X Wg^T, U = X Wu^T:
+//   dG = dH U act'(G),  dU = dH act(G)
+//   dX = dG Wg + dU Wu = [dG | dU] [Wg ; Wu]
+//   dWg = dG^T X, dWu = dU^T X: [dG | dU]^T X
+//
+// One pass makes [dG | dU] (16 bits a value), then two products read it: dX
+// along its rows, the weight gradients along its columns. Rounding dG and dU
+// to the operands' type is what lets the matrix cores multiply them; the error
+// it adds to a gradient (a half step of each of many independent terms) is the
+// size of that gradient's own last rounding. No operand is transposed or
+// repacked in memory: the products read X, [dG | dU] and the packed weights
+// through the transposing LDS reads.
+#include "ffn_tile.h"
+
+namespace bmm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// One thread: 8 columns of dG and of dU in one row. Read dH, G and U once, write
+// both halves: 10 bytes a column.
+template <int DT, int ACT>
+__global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__ dgu,
+                                                          const uint16_t* __restrict__ dh,
+                                                          const uint16_t* __restrict__ g,
+                                                          const uint16_t* __restrict__ u,
+                                                          int64_t n, int64_t F, int64_t Fp,
+                                                          int64_t ld) {
+  const int64_t stride = int64_t(gridDim.x) * kThreads;
+  const int64_t per_row = Fp / 8;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
+    const int64_t row = i / per_row, f = 8 * (i % per_row);
+    u32x4 og = {0, 0, 0, 0}, ou = {0, 0, 0, 0};
+    if (f < F) {
+      const u32x4 vh = *reinterpret_cast<const u32x4*>(dh + row * ld + f);
+      const u32x4 vg = *reinterpret_cast<const u32x4*>(g + row * ld + f);
+      const u32x4 vu = *reinterpret_cast<const u32x4*>(u + row * ld + f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float dg[2], du[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t sh = 16 * e;
+          const float h = half_bits_to_f32<DT>((vh[w] >> sh) & 0xffffu);
+          const float x = half_bits_to_f32<DT>((vg[w] >> sh) & 0xffffu);
+          const float y = half_bits_to_f32<DT>((vu[w] >> sh) & 0xffffu);
+          float a, slope;
+          act_and_slope<ACT>(x, a, slope);
+          dg[e] = h * y * slope;
+          du[e] = h * a;
+        }
+        og[w] = pack2<DT>(dg[0], dg[1]);
+        ou[w] = pack2<DT>(du[0], du[1]);
+      }
+    }
+    uint16_t* out = dgu + row * 2 * Fp + f;
+    *reinterpret_cast<u32x4*>(out) = og;
+    *reinterpret_cast<u32x4*>(out + Fp) = ou;
+  }
+}
+
+// The partial sums of a split product, added in order and rounded once. Rows
+// as in TileArgs: r < rows0 to d, row1 <= r < row1 + rows0 to d1.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void join_kernel(TileArgs p, int64_t n8) {
+  const int64_t stride = int64_t(gridDim.x) * kThreads;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n8; i += stride) {
+    const int64_t row = 8 * i / p.N, col = 8 * i % p.N;
+    const int64_t b = row / p.M, m = row % p.M;
+    const bool second = m >= p.row1;
+    const int64_t r = second ? m - p.row1 : m;
+    if (r >= p.rows0) continue;
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int s = 0; s < p.splits; ++s) {
+      const float* at = p.part + s * p.part_floats + 8 * i;
+      lo += load16f_nt(at);
+      hi += load16f_nt(at + 4);
+    }
+    const u32x4 o = {pack2<DT>(lo[0], lo[1]), pack2<DT>(lo[2], lo[3]), pack2<DT>(hi[0], hi[1]),
+                     pack2<DT>(hi[2], hi[3])};
+    uint16_t* d = static_cast<uint16_t*>(second ? p.d1 : p.d);
+    *reinterpret_cast<u32x4*>(d + (b * p.rows0 + r) * p.ldd + col) = o;
+  }
+}
+
+unsigned grid_for(int64_t n) {
+  const int64_t blocks = (n + kThreads - 1) / kThreads;
+  return unsigned(blocks < 8192 ? blocks : 8192);
+}
+
+template <int DT>
+hipError_t join(const TileArgs& a, hipStream_t s) {
+  const int64_t n8 = a.batch * a.M * a.N / 8;
+  hipLaunchKernelGGL(join_kernel<DT>, dim3(grid_for(n8)), dim3(kThreads), 0, s, a, n8);
+  return hipGetLastError();
+}
+
+template <int DT, int SRCA, int SRCB>
+hipError_t product(const TileArgs& a, hipStream_t s) {
+  hipError_t e = ffn::launch_tile<DT, SRCA, SRCB, ffn::kStore, 128, 128>(a, s);
+  if (e == hipSuccess && a.splits > 1) e = join<DT>(a, s);
+  return e;
+}
+
+}  // namespace
+
+hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
+                               const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
+                               int act, hipStream_t s) {
+  const int64_t Fp = (F + 31) / 32 * 32, n = rows * Fp / 8;
+  if (n == 0) return hipSuccess;
+  auto pick = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    switch (act) {
+      case BMM_ACT_SILU: return slopes_kernel<DT, BMM_ACT_SILU>;
+      case BMM_ACT_GELU: return slopes_kernel<DT, BMM_ACT_GELU>;
+      case BMM_ACT_GELU_TANH: return slopes_kernel<DT, BMM_ACT_GELU_TANH>;
+      default: return slopes_kernel<DT, BMM_ACT_RELU>;
+    }
+  };
+  auto kern = dtype == kBF16 ? pick(std::integral_constant<int, kBF16>{})
+                             : pick(std::integral_constant<int, kF16>{});
+  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld);
+  return hipGetLastError();
+}
+
+hipError_t launch_gated_dx(const TileArgs& a, int dtype, hipStream_t s) {
+  return dtype == kBF16 ? product<kBF16, ffn::kRows, ffn::kPackedT2>(a, s)
+                        : product<kF16, ffn::kRows, ffn::kPackedT2>(a, s);
+}
+
+hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
+  return dtype == kBF16 ? product<kBF16, ffn::kTrans, ffn::kTrans>(a, s)
+                        : product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
+}
+
+// Splits of a product's summed axis (K values). Tiles of 128 x 128 run two to
+// a CU; a split keeps at least 16 slabs of 32 values, and 32 partial sums at
+// most are joined.
+int ffn_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = batch * ((M + 127) / 128) * ((N + 127) / 128);
+  if (tiles == 0) return 1;
+  int64_t s = 512 / tiles;
+  const int64_t deep = K / 32 / 16;
+  if (s > deep) s = deep;
+  if (s > 32) s = 32;
+  return int(s < 1 ? 1 : s);
+}
+
+}  // namespace bmm

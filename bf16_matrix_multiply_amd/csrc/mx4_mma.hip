@@ -1,0 +1,17 @@
+// Products of 4-bit operands: D = A B^T, and the gated block
+// H = act(X Wg^T) * (X Wu^T), on the scaled 16x16x128 MFMA.
+#include "ffn_tile.h"
+
+namespace bmm {
+
+hipError_t launch_mx4_mma(const TileArgs& a, hipStream_t s) {
+  using namespace ffn;
+  return launch_tile<kMX4, kCodes, kCodes, kStore, 128, 128>(a, s);
+}
+
+hipError_t launch_mx4_gated(const TileArgs& a, hipStream_t s) {
+  using namespace ffn;
+  return launch_tile<kMX4, kCodes, kCodes2, kGated, 128, 128>(a, s);
+}
+
+}  // namespace bmm

@@ -45,6 +45,29 @@ Status check_splitk(const float* D, const uint32_t* A, const uint32_t* B, const 
                     int32_t atom_k, int32_t splits, const void* workspace,
                     int64_t workspace_bytes);
 
+// Feed-forward operators (validate_ffn.cpp).
+Status check_gated(const uint16_t* H, const uint16_t* G, const uint16_t* U, const uint16_t* X,
+                   const uint32_t* Wg, const uint32_t* Wu, const bmm_gated_desc* d);
+// Extents alone; `what` prefixes the messages.
+Status check_gated_desc(const bmm_gated_desc* d, const char* what);
+Status check_gated_backward(const uint16_t* dX, const uint16_t* dWg, const uint16_t* dWu,
+                            const uint16_t* dH, const uint16_t* G, const uint16_t* U,
+                            const uint16_t* X, const uint32_t* Wg, const uint32_t* Wu,
+                            const bmm_gated_desc* d, const void* workspace,
+                            int64_t workspace_bytes, int64_t need);
+// Bytes of a 4-bit operand's codes and scales, or -1 for invalid extents.
+int64_t mx4_codes_bytes(int64_t batch, int64_t rows, int64_t K);
+int64_t mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K);
+// Quantise (`mat` is read) or dequantise (`mat` is written).
+Status check_mx4_convert(const void* mat, const uint8_t* codes, const uint8_t* scales,
+                         int64_t batch, int64_t rows, int64_t K, int64_t ld, int32_t elem_type,
+                         const char* what);
+// Product (B1 null) or gated product (B0 = Wg, B1 = Wu).
+Status check_mx4_product(const void* D, const uint8_t* A, const uint8_t* As, const uint8_t* B0,
+                         const uint8_t* B0s, const uint8_t* B1, const uint8_t* B1s, bool gated,
+                         int64_t batch, int64_t M, int64_t N, int64_t K, int64_t ld, int32_t act,
+                         int32_t elem_type);
+
 // Largest image (bytes) one box repeat may stage through LDS.
 constexpr int64_t kBoxImageLimit = 65536;
 

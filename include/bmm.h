@@ -404,6 +404,160 @@ int bmm_splitk_suggested(int64_t batch, int64_t M_rep, int64_t N_rep, int64_t K_
  * bmm_kernel value), or < 0. */
 int bmm_select_kernel(int64_t batch, int64_t M_rep, int64_t N_rep, int64_t K_rep);
 
+/*
+ * ---- Feed-forward operators ----
+ *
+ * Activations and gradients are row-major matrices of 16-bit values (f16 or
+ * bf16 bits, named by dtype): (batch, rows, ld) with `ld` elements between
+ * rows and rows * ld between batches, ld a multiple of 8, base 16-byte
+ * aligned. Any number of rows is taken. Weights are packed B operands as
+ * bmm_pack_operand (atom_rows 8) lays them out, or 4-bit operands.
+ */
+
+/* Activations. GELU is x Phi(x); GELU_TANH is 0.5 x (1 + tanh(sqrt(2 / pi)
+ * (x + 0.044715 x^3))). */
+typedef enum {
+  BMM_ACT_SILU = 0,
+  BMM_ACT_GELU = 1,
+  BMM_ACT_GELU_TANH = 2,
+  BMM_ACT_RELU = 3
+} bmm_act;
+
+/*
+ * Extents of a gated feed-forward block.
+ *   batch  independent blocks (each with its own weights)
+ *   M      rows of X (tokens); any
+ *   F      width of the block, a multiple of 8, at most 2^20
+ *   K      width of X, a multiple of 16, below 2^22
+ *   ld_x   elements between rows of X: >= K, a multiple of 8, at most 2^21
+ *   ld_h   elements between rows of H, G, U and dH: >= F, a multiple of 8, at
+ *          most 2^21
+ *   dtype  bmm_dtype of every 16-bit value
+ *   act    bmm_act
+ */
+typedef struct {
+  int64_t batch;
+  int64_t M;
+  int64_t F;
+  int64_t K;
+  int64_t ld_x;
+  int64_t ld_h;
+  int32_t dtype;
+  int32_t act;
+} bmm_gated_desc;
+
+/*
+ * bmm_gated — H = act(G) * U with G = X Wg^T and U = X Wu^T, in one kernel.
+ *
+ * H      (batch, M, ld_h) written in the first F columns of each row.
+ * G, U   as H, or both NULL. When given they receive the projections, rounded
+ *        to dtype, which bmm_gated_backward takes; H is made from the
+ *        unrounded float32 projections either way.
+ * X      (batch, M, ld_x), the first K columns of each row are read.
+ * Wg, Wu (batch, F/8, K/16, 8, 8) packed words (bmm_pack_operand, atom_rows 8).
+ * The sums are float32; H, G and U are rounded once (nearest even). K = 0
+ * gives H = act(0) * 0 = 0. Zero batch, M or F is a no-op.
+ * Errors: BMM_EINVAL, BMM_EALIGN, BMM_EOVERLAP (outputs with each other or
+ * with an input; interleaved rows of one buffer are no overlap), BMM_EHIP.
+ */
+int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const uint32_t* Wg,
+              const uint32_t* Wu, const bmm_gated_desc* desc, void* stream);
+
+/*
+ * bmm_gated_backward — gradients of bmm_gated from dH and the kept projections.
+ *
+ *   dG = dH * U * act'(G), dU = dH * act(G)   (relu'(x) = 1 for x > 0, else 0)
+ *   dX = dG Wg + dU Wu;  dWg = dG^T X;  dWu = dU^T X
+ *
+ * dX         (batch, M, K) contiguous, or NULL when it is not wanted.
+ * dWg, dWu   (batch, F, K) contiguous and row-major, or both NULL. (M = 0
+ *            writes zeros, the empty sum; F = 0 does so for dX.)
+ * dH, G, U   (batch, M, ld_h); X (batch, M, ld_x); Wg, Wu as bmm_gated (may be
+ *            NULL when dX is).
+ * dG and dU are rounded to dtype before they are multiplied; sums are
+ * float32, each gradient is rounded once. The result is the same on every run.
+ * workspace  device memory of at least bmm_gated_backward_workspace_bytes(desc)
+ *            bytes, 16-byte aligned, overlapping nothing else; owned by the
+ *            caller, clobbered.
+ * Errors: as bmm_gated; BMM_EINVAL also for a missing or short workspace and
+ * when nothing is wanted.
+ */
+int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_t* dH,
+                       const uint16_t* G, const uint16_t* U, const uint16_t* X,
+                       const uint32_t* Wg, const uint32_t* Wu, const bmm_gated_desc* desc,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes bmm_gated_backward needs for these extents, or < 0. */
+int64_t bmm_gated_backward_workspace_bytes(const bmm_gated_desc* desc);
+
+/*
+ * 4-bit operands: microscaled floats (OCP Microscaling Formats v1.0, MXFP4).
+ *
+ * 32 neighbouring K values of a row share a scale 2^(byte - 127) (byte 255:
+ * NaN, the whole block stands for NaN); a value's code is a sign bit and an
+ * index into {0, 0.5, 1, 1.5, 2, 3, 4, 6}.
+ *
+ * codes   (batch, ceil(rows/16), ceil(K/128), 4, 16, 16) bytes:
+ *         [b, r, s, g, i, j] holds row 16 r + i, K values 128 s + 32 g + 2 j
+ *         (low half) and 128 s + 32 g + 2 j + 1 (high half).
+ * scales  (batch, ceil(rows/16), ceil(K/512), 4, 16, 4) bytes:
+ *         [b, r, q, g, i, t] scales row 16 r + i, K values
+ *         512 q + 128 t + 32 g .. + 31.
+ * Both contiguous, codes and scales 16-byte aligned. Codes and scales of rows
+ * and K values outside the matrix are zero. The same layout serves as A and
+ * as B. K is a multiple of 32, below 2^22.
+ */
+int64_t bmm_mx4_codes_bytes(int64_t batch, int64_t rows, int64_t K);
+int64_t bmm_mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K);
+
+/*
+ * bmm_mx4_quantize — a row-major matrix to a 4-bit operand.
+ *
+ * Per block: e = floor(log2(largest magnitude)) - 2, at least -127; the scale
+ * byte is e + 127 and each code is x / 2^e rounded to the nearest value, ties
+ * to the even code, at most 6 in magnitude. A block with a NaN or an infinity
+ * gets scale byte 255; a block of zeros gets scale byte 0.
+ * src  (batch, rows, ld_src) values of elem_type (BMM_ELEM_F32, _F16 or
+ *      _BF16), batch stride rows * ld_src, 16-byte aligned; ld_src >= K and a
+ *      multiple of 8. Padding of codes and scales is written too.
+ * Zero batch, rows or K is a no-op.
+ * Errors: BMM_EINVAL, BMM_EALIGN, BMM_EOVERLAP, BMM_EHIP.
+ */
+int bmm_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t batch, int64_t rows,
+                     int64_t K, int64_t ld_src, int32_t elem_type, void* stream);
+
+/* bmm_mx4_dequantize — the values of a 4-bit operand, rounded to elem_type
+ * (exact but for f16's range and values below the type's smallest). dst as
+ * src above; columns from K on are not written. */
+int bmm_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales, int64_t batch,
+                       int64_t rows, int64_t K, int64_t ld_dst, int32_t elem_type, void* stream);
+
+/*
+ * bmm_mx4_mma — D = A * B^T over 4-bit operands.
+ *
+ * D  (batch, M, ld_d) of elem_type (BMM_ELEM_F32, _F16 or _BF16), written in
+ *    the first N columns; ld_d >= N, a multiple of 8, 16-byte aligned.
+ * A  4-bit operand of M rows, B of N rows, both of K values; N a multiple of 8.
+ * Sums are float32, rounded once. K = 0 gives zeros; zero batch, M or N is a
+ * no-op.
+ * Errors: BMM_EINVAL, BMM_EALIGN, BMM_EOVERLAP, BMM_EHIP.
+ */
+int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* B_codes,
+                const uint8_t* B_scales, int64_t batch, int64_t M, int64_t N, int64_t K,
+                int64_t ld_d, int32_t elem_type, void* stream);
+
+/*
+ * bmm_mx4_gated — H = act(X Wg^T) * (X Wu^T) over 4-bit operands.
+ *
+ * H  (batch, M, ld_h) of elem_type BMM_ELEM_F16 or BMM_ELEM_BF16, written in
+ *    the first F columns; X of M rows, Wg and Wu of F rows, all of K values; F
+ *    a multiple of 8. Otherwise as bmm_mx4_mma.
+ */
+int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
+                  const uint8_t* Wg_codes, const uint8_t* Wg_scales, const uint8_t* Wu_codes,
+                  const uint8_t* Wu_scales, int64_t batch, int64_t M, int64_t F, int64_t K,
+                  int64_t ld_h, int32_t act, int32_t elem_type, void* stream);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char* bmm_last_error(void);
 
