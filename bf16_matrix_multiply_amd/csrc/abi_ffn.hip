@@ -38,17 +38,17 @@ int64_t padded_width(int64_t F) { return (F + 31) / 32 * 32; }
 // one product at a time.
 struct BackwardPlan {
   int64_t slopes_bytes, need;
-  int dx_splits, dw_splits;
+  bmm::TilePlan dx, dw;
 };
 
 BackwardPlan plan_backward(const bmm_gated_desc& d) {
   BackwardPlan p;
   const int64_t Fp2 = 2 * padded_width(d.F);
   p.slopes_bytes = (d.batch * d.M * Fp2 * 2 + 255) / 256 * 256;
-  p.dx_splits = bmm::ffn_splits(d.batch, d.M, d.K, Fp2);
-  p.dw_splits = bmm::ffn_splits(d.batch, Fp2, d.K, d.M);
-  const int64_t dx = p.dx_splits > 1 ? p.dx_splits * d.batch * d.M * d.K * 4 : 0;
-  const int64_t dw = p.dw_splits > 1 ? p.dw_splits * d.batch * Fp2 * d.K * 4 : 0;
+  p.dx = bmm::plan_tiles(d.batch, d.M, d.K, Fp2 / 32, true);
+  p.dw = bmm::plan_tiles(d.batch, Fp2, d.K, (d.M + 31) / 32, true);
+  const int64_t dx = p.dx.splits > 1 ? p.dx.splits * d.batch * d.M * d.K * 4 : 0;
+  const int64_t dw = p.dw.splits > 1 ? p.dw.splits * d.batch * Fp2 * d.K * 4 : 0;
   p.need = p.slopes_bytes + (dx > dw ? dx : dw);
   return p;
 }
@@ -87,6 +87,7 @@ int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const ui
     a.ldd = d.ld_h;
     a.a_bs = d.M * d.ld_x;
     a.b_bs = d.F * d.K;
+    a.tile = bmm::plan_tiles(d.batch, d.M, 2 * d.F, d.K / 32, false).tile;
     return hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
                       "gated launch");
   });
@@ -136,7 +137,8 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.b_bs = d.F * d.K;
       a.b_sum = Fp;
       a.b_rows = d.F;
-      a.splits = plan.dx_splits;
+      a.tile = plan.dx.tile;
+      a.splits = plan.dx.splits;
       a.part = part;
       a.part_floats = d.batch * d.M * d.K;
       rc = hip_status(bmm::launch_gated_dx(a, d.dtype, s), "gated_backward dX launch");
@@ -156,7 +158,8 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.ldb = d.ld_x;
       a.a_bs = d.M * 2 * Fp;
       a.b_bs = d.M * d.ld_x;
-      a.splits = plan.dw_splits;
+      a.tile = plan.dw.tile;
+      a.splits = plan.dw.splits;
       a.part = part;
       a.part_floats = d.batch * 2 * Fp * d.K;
       rc = hip_status(bmm::launch_gated_dw(a, d.dtype, s), "gated_backward dW launch");
@@ -228,6 +231,7 @@ int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const 
     a.bs_bs = bmm::mx4_scales_bytes(1, N, K);
     a.out_type = elem_type;
     a.splits = 1;
+    a.tile = bmm::plan_tiles(batch, M, N, K / 128, false).tile;
     return hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
   });
 }
@@ -262,6 +266,7 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
     a.act = act;
     a.out_type = elem_type;
     a.splits = 1;
+    a.tile = bmm::plan_tiles(batch, M, 2 * F, K / 128, false).tile;
     return hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
                       "mx4_gated launch");
   });

@@ -15,6 +15,9 @@ namespace bmm {
 // with a scale for every 32 K values.
 enum : int { kMX4 = 2 };
 
+// Rows x columns of a product's tile (gated: columns of both weights).
+enum TileSize : int { kTile128, kTile256x128, kTile256 };
+
 // One product D = A * B^T on MFMA tiles. Which fields count depends on how
 // the operands lie in memory and on the epilogue (ffn_tile.h).
 struct TileArgs {
@@ -36,6 +39,7 @@ struct TileArgs {
   int64_t b_rows;           // ... and how many of them exist (the rest count as zero)
   // store: rows r < rows0 go to d, rows row1 <= r < row1 + rows0 to d1, others nowhere
   int64_t rows0, row1;
+  int tile;                 // a TileSize
   int act;
   int out_type;             // bmm_elem_type: F32, F16 or BF16
   // split sum (store only): split s of `splits` takes slabs [s n / S, (s + 1) n / S) of the
@@ -62,8 +66,11 @@ hipError_t launch_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t*
 hipError_t launch_mx4_mma(const TileArgs& a, hipStream_t s);
 hipError_t launch_mx4_gated(const TileArgs& a, hipStream_t s);
 
-// Partial sums a split product wants: enough (tiles x splits) for the chip.
-int ffn_splits(int64_t batch, int64_t M, int64_t N, int64_t K);
+// How a product of M rows, N columns (gated: of both weights) and so many slabs is cut.
+struct TilePlan {
+  int tile, splits;
+};
+TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split);
 
 // ---- activations ----
 // exp is the hardware's 2^x (1 ulp) of x log2(e); the product's rounding makes

@@ -21,19 +21,35 @@
 //
 // Staging: every wave moves 1 KB pieces from memory to LDS with direct loads
 // (lane l's 16 bytes land at 16 l). The lanes' source addresses arrange the
-// piece, so that the reads that follow are spread over all banks:
-// - packed and 4-bit: the piece is a fragment in lane order;
-// - rows: 16 rows x 64 bytes; the 16-byte chunk c of row r lies at chunk
-//   c ^ (r / 4 % 4), so the 16 lanes that read chunk c of 16 rows meet 16
-//   different bank groups;
+// piece, so that 16 neighbouring lanes ask for whole 128-byte lines (a line
+// asked for by halves costs the cache two requests: with 64 bytes of a row in
+// a piece the gated block took 800 us for 8192 x 4096 -> 8192, and a half more
+// line requests), and so that the reads that follow are spread over all banks.
+// A ds_read_b128 serves 16 lanes a cycle, of lanes 0-31 first 0-3, 12-15 and
+// 20-27, then the others; a ds_read_b64 lanes 0-31, then 32-63. No conflicts
+// are counted for any of these:
+// - 4-bit: the piece is a fragment in lane order;
+// - packed: the piece is two atom rows of 512 bytes as they are;
+// - rows: 8 rows x 128 bytes, two slabs at once; the 16-byte chunk c of row r
+//   lies at chunk c ^ rows_swizzle(r);
 // - transposed: [64-column block][32 summed rows][128 bytes], read with the
 //   hardware's transposing LDS read (ds_read_b64_tr_b16: of 16 lanes, lane
 //   4 k + a reads four columns 4a .. 4a + 3 of summed row k, and lane i
 //   receives column i of the four rows). Pairs of 16-byte chunks of summed row
-//   k are exchanged by k's bits 1 and 3, so that the eight rows which half a
-//   wave reads lie in different banks.
+//   k are exchanged by k's bits 1 and 3;
+// - transposed packed: the piece is four atoms (8 summed rows x 64 columns) as
+//   they are, with the two 128-byte halves of an atom exchanged for every other
+//   8 summed rows; read as above.
 // What lies outside the matrices is read as zero: such lanes are given an
 // address past the buffer's end, so no memory is touched.
+//
+// Schedule: a ring of four stages. Slab s is multiplied from registers while
+// the wave reads the fragments of slab s + 1 from LDS into its second register
+// set and sends the loads of slab s + 3 into the stage that slab s - 1 has left;
+// reads and loads are placed between the MFMAs, and one barrier a slab, after
+// its first two MFMAs, publishes the loads that every wave waited for at the end
+// of the slab before. The loop runs whole turns of the ring: slabs past the end
+// read as zeros.
 #pragma once
 
 #include <type_traits>
@@ -69,6 +85,23 @@ constexpr int waitcnt_imm(int vm, int lgkm) {
   return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | ((lgkm & 15) << 8);
 }
 
+// f(integral_constant i) for i in [A, B).
+template <int A, int B, class Fn>
+__device__ __forceinline__ void static_for(Fn fn) {
+  if constexpr (A < B) {
+    fn(std::integral_constant<int, A>{});
+    static_for<A + 1, B>(fn);
+  }
+}
+
+// Which of n items that are spread over `span` places (at the start of their
+// shares, or with `middle` in the middle) falls on this place; -1: none.
+constexpr int item_at(int place, int n, int middle, int span) {
+  for (int i = 0; i < n; ++i)
+    if ((2 * i + middle) * span / (2 * n) == place) return i;
+  return -1;
+}
+
 struct TileAt {
   int64_t b, mt, nt;
 };
@@ -91,42 +124,53 @@ __device__ __forceinline__ TileAt tile_at(int64_t t, int64_t MT, int64_t NT) {
   return {b, first_m + v % gm, v / gm};
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(kOutOfRange), kBufferFlags);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, uint32_t bytes = kOutOfRange) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, int(bytes), kBufferFlags);
 }
+
+// The exchange of 16-byte chunks in the row-major image: by r / 2: 0, 2, 0, 2, 4, 6, 4, 6.
+__device__ __forceinline__ int rows_swizzle(int r) { return (r & 2) | ((r >> 1) & 4); }
 
 // Bits 1 and 3 of a summed row's index within its slab: the exchange of chunk
 // pairs of the transposed image.
 __device__ __forceinline__ int trans_swizzle(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
 
-// The loads of one operand: piece f = 4 r + wave of T / 16, r < T / 64.
+// Slabs that one round of an operand's loads brings.
+constexpr int slabs_a_load(int src) { return src == kRows ? 2 : 1; }
+
+// The loads of one operand: 1 KB piece 4 r + wave of T / 16 (rows: of T / 8).
 template <int SRC, int T>
 struct Loader {
+  static constexpr int kSlabs = slabs_a_load(SRC), kLoads = T / 64 * kSlabs;
   const char* base0;       // slab 0, source 0 (or this wave's source)
   const char* base1;       // kPackedT2: slab 0 of source 1
-  int64_t step;            // bytes from slab to slab
-  int64_t n_sum;           // summed values (kPackedT2: of one source)
+  int64_t step;            // bytes from one round to the next
+  int64_t end;             // summed values to take (kPackedT2: slabs)
+  int64_t per;             // kPackedT2: slabs of one source
   int64_t n_rows;          // kPackedT2: summed values that exist in one source
-  int k_lane;              // this lane's first summed value within a slab
-  uint32_t off[4];         // fixed size: T / 64 are used
+  int k_lane;              // this lane's first summed value within a round
+  uint32_t off[4];         // fixed size: T / 64 are used (rows: one)
+  uint32_t bytes;          // rows: size of the buffer, past which no row exists
+  uint32_t piece;          // rows: bytes from a piece to this wave's next one
 
-  // r0: first row (column of D for B) of the tile; n: rows that exist.
+  // r0: first row (column of D for B) of the tile; n: rows that exist; slab_end:
+  // slabs from there on read as zeros.
   __device__ __forceinline__ void init(const TileArgs& p, const void* s0, const void* s1,
                                        int64_t batch_off, int64_t ld, int64_t r0, int64_t n,
-                                       int lane, int wave) {
-    n_sum = p.K;
-    n_rows = 0;
+                                       int64_t slab_end, int lane, int wave) {
+    end = slab_end * slab_values(SRC) < p.K ? slab_end * slab_values(SRC) : p.K;
+    per = n_rows = 0;
     base1 = nullptr;
+    bytes = kOutOfRange;
+    piece = 0;
     if constexpr (SRC == kRows) {
-      const int row = lane >> 2, c = (lane & 3) ^ ((lane >> 4) & 3);
+      const int row = 8 * wave + (lane >> 3), c = (lane & 7) ^ rows_swizzle(row & 15);
       k_lane = 8 * c;
-      step = 64;
+      step = 128;
       base0 = static_cast<const char*>(s0) + 2 * (batch_off + r0 * ld);
-#pragma unroll
-      for (int r = 0; r < T / 64; ++r) {
-        const int i = 16 * (4 * r + wave) + row;
-        off[r] = r0 + i < n ? uint32_t(i * ld * 2 + 16 * c) : kOutOfRange;
-      }
+      off[0] = uint32_t(row * ld * 2 + 16 * c);
+      piece = uint32_t(64 * ld);
+      bytes = uint32_t((n - r0 < T ? n - r0 : T) * ld * 2);   // ld <= 2^21: at most 2^30
     } else if constexpr (SRC == kTrans) {
       k_lane = 8 * wave + (lane >> 3);
       const int e = (lane & 7) ^ (2 * trans_swizzle(k_lane));
@@ -138,31 +182,26 @@ struct Loader {
                                          : kOutOfRange;
     } else if constexpr (SRC == kPackedT2) {
       // one atom row of 8 summed values a wave; n columns make n / 16 atoms in it
-      const int kk = lane >> 3;
-      k_lane = 8 * wave + kk;
-      const int e = (lane & 7) ^ (2 * trans_swizzle(k_lane));
+      const int x = lane ^ (8 * (wave & 1));
+      k_lane = 8 * wave + ((x & 15) >> 1);
       step = 64 * n;
-      n_sum = p.b_sum;
+      end = slab_end;
+      per = p.b_sum / 32;
       n_rows = p.b_rows;
       base0 = static_cast<const char*>(s0) + 2 * batch_off + 16 * r0;
       base1 = static_cast<const char*>(s1) + 2 * batch_off + 16 * r0;
 #pragma unroll
       for (int r = 0; r < T / 64; ++r)
-        off[r] = r0 + 64 * r + 8 * e < n
-                     ? uint32_t(wave * n * 16 + (4 * r + (e >> 1)) * 256 + kk * 32 + (e & 1) * 16)
-                     : kOutOfRange;
+        off[r] = r0 + 64 * r + 16 * (lane >> 4) < n ? uint32_t(wave * n * 16 + 1024 * r + 16 * x)
+                                                    : kOutOfRange;
     } else if constexpr (SRC == kPacked2) {
-      const int c = lane & 15, g = lane >> 4;
-      k_lane = 8 * g;
+      k_lane = (lane & 16) + 8 * (lane & 1);
       step = 512;
       base0 = static_cast<const char*>(wave & 1 ? s1 : s0) + 2 * (batch_off + r0 * p.K);
 #pragma unroll
       for (int r = 0; r < T / 64; ++r) {
-        const int cb = 2 * r + (wave >> 1);   // 16-column block of this piece
-        off[r] = r0 + 16 * cb + (c & 8) < n
-                     ? uint32_t((2 * cb + (c >> 3)) * p.K * 16 + (g >> 1) * 256 + (c & 7) * 32 +
-                                (g & 1) * 16)
-                     : kOutOfRange;
+        const int half = 2 * (2 * r + (wave >> 1)) + (lane >> 5);   // 8-column atom row
+        off[r] = r0 + 8 * half < n ? uint32_t(half * p.K * 16 + 16 * (lane & 31)) : kOutOfRange;
       }
     } else {
       const int64_t row_bytes = (p.K + 127) / 128 * 1024;   // a group of 16 rows
@@ -178,73 +217,123 @@ struct Loader {
     }
   }
 
-  // Slab k into the operand's stage (T / 16 pieces of 1 KB).
-  __device__ __forceinline__ void issue(char* stage, int64_t k, int wave) const {
-    constexpr int kValues = slab_values(SRC);
-    bool ok;
+  // Where round k starts, and whether this lane's summed values exist.
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t round(int64_t k, bool& ok) const {
+    constexpr int kValues = kSlabs * slab_values(SRC);
+    int64_t left;        // summed values from this round on
     const char* at;
     if constexpr (SRC == kPackedT2) {
-      const int64_t per = n_sum / 32;
       const int64_t j = k < per ? k : k - per;
       at = (k < per ? base0 : base1) + j * step;
-      ok = k < 2 * per && 32 * j + k_lane < n_rows;
+      left = k < end ? n_rows - 32 * j : 0;
     } else {
       at = base0 + k * step;
-      ok = kValues * k + k_lane < n_sum;
+      left = end - kValues * k;
     }
-    const __amdgpu_buffer_rsrc_t rsrc = buffer(at);
-#pragma unroll
-    for (int r = 0; r < T / 64; ++r)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(stage + 1024 * (4 * r + wave)),
-                                               16, ok ? off[r] : kOutOfRange, 0, 0, 0);
+    ok = k_lane < int(left < kValues ? left : kValues);
+    return buffer(at, bytes);
+  }
+  // This wave's r-th piece.
+  __device__ __forceinline__ void load(char* stage, __amdgpu_buffer_rsrc_t rsrc, bool ok, int r,
+                                       int wave) const {
+    const uint32_t o = SRC == kRows ? (ok ? off[0] : 1u << 30) + r * piece
+                                    : ok ? off[r] : kOutOfRange;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(stage + 1024 * (4 * r + wave)), 16,
+                                             o, 0, 0, 0);
   }
 };
 
-// This lane's 16 bytes of fragment f (rows 16 f .. of the tile) in a stage.
+// This lane's 16 bytes of fragment f (rows 16 f .. of the tile) in a stage;
+// rows: of slab h of the stage's two.
 template <int SRC>
 struct Reader {
-  int base;       // byte offset of the lane within a piece
-  int pair[4];    // transposed: the four exchanges of chunk pairs
+  int at[4];      // byte offset of the lane within a piece; rows: by h;
+                  // transposed: of the four exchanges of chunk pairs
+  int at4[4];     // transposed: four summed rows on
 
   __device__ __forceinline__ void init(int lane) {
+    const int i = lane & 15, g = lane >> 4;
     if constexpr (SRC == kRows) {
-      const int m = lane & 15;
-      base = 16 * (4 * m + ((lane >> 4) ^ ((m >> 2) & 3)));
-    } else if constexpr (SRC == kTrans || SRC == kPackedT2) {
-      const int i = lane & 15, k = 8 * (lane >> 4) + (i >> 2), a = i & 3;
-      base = 128 * k + 16 * (a >> 1) + 8 * (a & 1);
+      at[0] = 128 * i + 16 * (g ^ rows_swizzle(i));
+      at[1] = at[0] ^ 64;
+    } else if constexpr (SRC == kTrans) {
+      const int k = 8 * g + (i >> 2);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) pair[b] = 32 * (b ^ trans_swizzle(k));
+      for (int b = 0; b < 4; ++b) {
+        at[b] = 128 * k + 8 * (i & 3) + 32 * (b ^ trans_swizzle(k));
+        at4[b] = at[b] + 512;
+      }
+    } else if constexpr (SRC == kPackedT2) {
+      at[0] = 1024 * g + ((8 * i) ^ (128 * (g & 1)));
+      at4[0] = at[0] ^ 128;
+    } else if constexpr (SRC == kPacked2) {
+      at[0] = 512 * (i >> 3) + 256 * (g >> 1) + 32 * (i & 7) + 16 * (g & 1);
     } else {
-      base = 16 * lane;
+      at[0] = 16 * lane;
+    }
+    if constexpr (SRC == kTrans || SRC == kPackedT2) {
+      // kept apart: the compiler follows an address only a few steps back to
+      // its stage, and waits for every load in flight where it cannot
+#pragma unroll
+      for (int b = 0; b < (SRC == kTrans ? 4 : 1); ++b) asm volatile("" : "+v"(at4[b]));
     }
   }
 
-  __device__ __forceinline__ u32x4 read(const char* stage, int f) const {
+  __device__ __forceinline__ u32x4 read(const char* stage, int f, int h) const {
     if constexpr (SRC == kTrans || SRC == kPackedT2) {
-      const char* at = stage + 4096 * (f >> 2) + pair[f & 3] + base;
+      const int b = SRC == kTrans ? f & 3 : 0;
+      const int block = 4096 * (f >> 2) + (SRC == kPackedT2 ? 256 * (f & 3) : 0);
       const u32x2 lo = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at));
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(stage + (block + at[b]))));
       const u32x2 hi = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + 512)));
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(stage + (block + at4[b]))));
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    } else if constexpr (SRC == kRows) {
+      return *(const volatile lds_u32x4*)(stage + (2048 * f + at[h]));
     } else {
-      return *(const volatile lds_u32x4*)(stage + 1024 * f + base);
+      return *(const volatile lds_u32x4*)(stage + (1024 * f + at[0]));
     }
   }
 };
 
-// Scales of 16-row group r16 for four slabs: one word a lane.
-__device__ __forceinline__ const uint32_t* scale_words(const uint8_t* scales, int64_t batch_off,
-                                                       int64_t K, int64_t r16, int lane) {
-  return reinterpret_cast<const uint32_t*>(scales + batch_off +
-                                           r16 * ((K + 511) / 512) * 256) + lane;
-}
+// Scale words of a tile's 16-row groups (a word a lane holds four slabs' scales).
+struct Scales {
+  __amdgpu_buffer_rsrc_t at;   // the tile's first group
+  int64_t row_bytes;           // a group
+  int64_t end;                 // words of a lane in a group
+  int last;                    // last group that exists, counted from the tile's first one
+  __device__ __forceinline__ void init(const uint8_t* s, int64_t batch_off, int64_t K, int64_t r0,
+                                       int64_t n) {
+    end = (K + 511) / 512;
+    row_bytes = end * 256;
+    at = buffer(s + batch_off + r0 / 16 * row_bytes, end ? kOutOfRange : 0);
+    const int64_t l = (n + 15) / 16 - 1 - r0 / 16;
+    last = l < 255 ? int(l) : 255;
+  }
+  // Group i (one past the matrix reads its last one; its outputs are not
+  // stored), slabs 4 q .. 4 q + 3 (past the end: the last word, not used).
+  __device__ __forceinline__ uint32_t word(int i, int64_t q, int lane) const {
+    const int64_t w = q < end ? q : end - 1;
+    return __builtin_amdgcn_raw_buffer_load_b32(at, 4 * lane,
+                                                int((i < last ? i : last) * row_bytes + 256 * w), 0);
+  }
+};
 
+// acc += b a^T over 32 values, in place. Written out, since the compiler gives
+// the result of its own form other registers than the sum it starts from; with
+// all 256 accumulator registers in use it then moved a third of them about in
+// every slab. Nothing but these instructions may touch the accumulators between
+// settle() and settle(): the compiler does not know that the results take time.
 template <int DT>
-__device__ __forceinline__ f32x4 mfma(u32x4 b, u32x4 a, f32x4 acc) {
-  return mfma_16x16x32<DT>(b, a, acc);
+__device__ __forceinline__ void mfma(u32x4 b, u32x4 a, f32x4& acc) {
+  if constexpr (DT == kBF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
+// Enough wait states for any MFMA's result to be read, or for accumulators that
+// were just written to be used (18 are needed at most).
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7"); }
 // 16 x 16 x 128 with 4-bit operands; byte SEL of each lane's scale word scales
 // its 32 values.
 template <int SEL>
@@ -324,13 +413,23 @@ __device__ __forceinline__ void gated_blocks(const TileArgs& p, int64_t b, int64
   }
 }
 
+// 256 rows: one workgroup a CU (a wave's 64 accumulators of 4 floats fill the
+// accumulator registers, so 128 x 128 of D come from 16 fragment reads);
+// 128 x 128: two workgroups a CU.
 template <int DT, int SRCA, int SRCB, int EPI, int TM, int TN>
-__global__ __launch_bounds__(kTileWaves* kWave) void ffn_tile_kernel(TileArgs p, int64_t n_tiles,
-                                                                     int64_t MT, int64_t NT) {
+__global__ __launch_bounds__(kTileWaves* kWave)
+__attribute__((amdgpu_waves_per_eu(TM == 256 ? 1 : 2, TM == 256 ? 1 : 2)))
+void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
   constexpr int kBM = TM / 32, kBN = TN / 32;   // 16-row and 16-column blocks a wave
   constexpr int kCols = EPI == kGated ? TN / 2 : TN;   // columns of D a tile
   static_assert((EPI == kGated) == two_sources(SRCB), "gated: two sources of B");
-  __shared__ __attribute__((aligned(1024))) char sa[TM * 64], sb[TN * 64];
+  // The ring. Separate objects, so that the compiler can tell the stages apart;
+  // with rows, which come two slabs at a time, A's stages 0 and 1 are one, and 2
+  // and 3.
+  constexpr bool kPairs = Loader<SRCA, TM>::kSlabs == 2;
+  __shared__ __attribute__((aligned(1024))) char b0[TN * 64], b1[TN * 64], b2[TN * 64], b3[TN * 64];
+  __shared__ __attribute__((aligned(1024))) char a0[TM * (kPairs ? 128 : 64)],
+      a2[TM * (kPairs ? 128 : 64)], a1[kPairs ? 16 : TM * 64], a3[kPairs ? 16 : TM * 64];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -340,74 +439,153 @@ __global__ __launch_bounds__(kTileWaves* kWave) void ffn_tile_kernel(TileArgs p,
   const int64_t split = work / n_tiles;
   const TileAt t = tile_at(work % n_tiles, MT, NT);
   const int64_t m0 = t.mt * TM, n0 = t.nt * kCols;
+  constexpr int kValues = slab_values(SRCA);
+  const int64_t slabs = (p.K + kValues - 1) / kValues;
+  // (a split starts at an even slab: rows come two slabs at a time)
+  const int64_t pairs = (slabs + 1) / 2, s0 = 2 * (split * pairs / splits);
+  const int64_t s1 = split + 1 < splits ? 2 * ((split + 1) * pairs / splits) : slabs;
 
   Loader<SRCA, TM> la;
   Loader<SRCB, TN> lb;
-  la.init(p, p.a, nullptr, t.b * p.a_bs, p.lda, m0, p.M, lane, wave);
-  lb.init(p, p.b0, p.b1, t.b * p.b_bs, p.ldb, n0, p.N, lane, wave);
+  la.init(p, p.a, nullptr, t.b * p.a_bs, p.lda, m0, p.M, s1, lane, wave);
+  lb.init(p, p.b0, p.b1, t.b * p.b_bs, p.ldb, n0, p.N, s1, lane, wave);
   Reader<SRCA> ra;
   Reader<SRCB> rb;
   ra.init(lane);
   rb.init(lane);
+  constexpr int kLoadsA = Loader<SRCA, TM>::kLoads, kLoadsB = Loader<SRCB, TN>::kLoads;
+  auto issue_a = [&](char* stage, int64_t k) {
+    bool ok;
+    const auto at = la.round(k, ok);
+#pragma unroll
+    for (int r = 0; r < kLoadsA; ++r) la.load(stage, at, ok, r, wave);
+  };
+  auto issue_b = [&](char* stage, int64_t k) {
+    bool ok;
+    const auto at = lb.round(k, ok);
+#pragma unroll
+    for (int r = 0; r < kLoadsB; ++r) lb.load(stage, at, ok, r, wave);
+  };
 
+  // 4-bit: this wave's scale words of four slabs, and of the next four
+  Scales ca, cb0, cb1;
+  uint32_t xa[8], xb[8], ya[8], yb[8];
+  constexpr int kWords = DT == kMX4 ? kBM + kBN : 0;
+  auto load_scale = [&](auto word, int64_t q) {   // one of kWords
+    constexpr int i = decltype(word)::value, j = i - kBM;
+    if constexpr (i < kBM) ya[i] = ca.word(kBM * wm + i, q, lane);
+    else if constexpr (EPI == kGated)
+      yb[j] = (j & 1 ? cb1 : cb0).word((kBN * wn + j) >> 1, q, lane);
+    else yb[j] = cb0.word(kBN * wn + j, q, lane);
+  };
+  auto take_scales = [&]() {
+    if constexpr (DT == kMX4) {
+#pragma unroll
+      for (int i = 0; i < kBM; ++i) xa[i] = ya[i];
+#pragma unroll
+      for (int j = 0; j < kBN; ++j) xb[j] = yb[j];
+    }
+  };
+  if constexpr (DT == kMX4) {
+    ca.init(p.as, t.b * p.as_bs, p.K, m0, p.M);
+    cb0.init(p.bs0, t.b * p.bs_bs, p.K, n0, p.N);
+    if constexpr (EPI == kGated) cb1.init(p.bs1, t.b * p.bs_bs, p.K, n0, p.N);
+  }
+
+  // Pinned to accumulator registers one by one: equal starting values would be
+  // merged, and the loop would then copy them.
   f32x4 acc[8][8];   // [16-row block][16-column block], kBM x kBN used
 #pragma unroll
   for (int i = 0; i < kBM; ++i)
 #pragma unroll
-    for (int j = 0; j < kBN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // 4-bit: where this wave's scale words start, one pointer a 16-row group
-  // (groups outside read the last one; their outputs are not stored)
-  const uint32_t* wa[8];
-  const uint32_t* wb[8];
-  if constexpr (DT == kMX4) {
-#pragma unroll
-    for (int i = 0; i < kBM; ++i) {
-      const int64_t r = m0 / 16 + kBM * wm + i, last = (p.M + 15) / 16 - 1;
-      wa[i] = scale_words(p.as, t.b * p.as_bs, p.K, r < last ? r : last, lane);
-    }
-#pragma unroll
     for (int j = 0; j < kBN; ++j) {
-      const int cb = EPI == kGated ? (kBN * wn + j) >> 1 : kBN * wn + j;
-      const int64_t r = n0 / 16 + cb, last = (p.N + 15) / 16 - 1;
-      wb[j] = scale_words(EPI == kGated && (j & 1) ? p.bs1 : p.bs0, t.b * p.bs_bs, p.K,
-                          r < last ? r : last, lane);
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      asm volatile("" : "+a"(v));
+      acc[i][j] = v;
     }
-  }
+  settle();
 
-  constexpr int kValues = slab_values(SRCA);
-  const int64_t slabs = (p.K + kValues - 1) / kValues;
-  const int64_t s0 = split * slabs / splits, s1 = (split + 1) * slabs / splits;
-  for (int64_t s = s0; s < s1; ++s) {
-    la.issue(sa, s, wave);
-    lb.issue(sb, s, wave);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-    __syncthreads();
-    u32x4 fa[8], fb[8];
+  u32x4 F0[16], F1[16];   // one slab's fragments: B's kBN, then A's kBM
+  const int64_t a_first = kPairs ? s0 / 2 : s0;   // A's first round
+  auto read = [&](const char* sa, int h, const char* sb, u32x4 (&F)[16], int i) {
+    F[i] = i < kBN ? rb.read(sb, kBN * wn + i, 0) : ra.read(sa, kBM * wm + i - kBN, h);
+  };
+  // Slab s, the ring's turn-th: fragments Fc; reads slab s + 1 from (na, nb) to
+  // Fn; loads slab s + 3 to (ta, tb) (rows: slabs s + 3 and s + 4, in odd turns).
+  auto slab = [&](auto turn, int64_t s, const char* na, const char* nb, char* ta, char* tb,
+                  const u32x4 (&Fc)[16], u32x4 (&Fn)[16]) {
+    constexpr int SEL = decltype(turn)::value;
+    auto mma = [&](int i) {
+      const int r = i / kBN, c = i % kBN;
+      if constexpr (DT == kMX4)
+        acc[r][c] = mfma_mx4<SEL>(Fc[c], Fc[kBN + r], xb[c], xa[r], acc[r][c]);
+      else
+        mfma<DT>(Fc[c], Fc[kBN + r], acc[r][c]);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    mma(0);
+    mma(1);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    // After the barrier the reads are spread over the first part of the MFMAs
+    // (they have to be back at the end of the slab), the loads over all of them:
+    // sent in a burst they would wait for each other, and the MFMAs behind them.
+    constexpr int kNowA = !kPairs || SEL % 2 == 1 ? kLoadsA : 0, kNow = kNowA + kLoadsB;
+    bool oka, okb;
+    const auto la_at = la.round(kPairs ? (s - s0 + 3) / 2 + a_first : s + 3, oka);
+    const auto lb_at = lb.round(s + 3, okb);
+    constexpr int kMfmas = kBM * kBN, kFrags = kBM + kBN;
+    constexpr int kVmem = kNow + (SEL == 0 ? kWords : 0);
+    static_for<2, kMfmas>([&](auto at) {
+      constexpr int i = decltype(at)::value;
+      mma(i);
+      constexpr int f = item_at(i - 2, kFrags, 0, kMfmas * 3 / 4), v = item_at(i - 2, kVmem, 1, kMfmas - 2);
+      if constexpr (f >= 0) read(na, (SEL + 1) % 2, nb, Fn, f);
+      if constexpr (v >= kNow)
+        load_scale(std::integral_constant<int, v - kNow>{}, (s >> 2) + 1);
+      else if constexpr (v >= kNowA)
+        lb.load(tb, lb_at, okb, v - kNowA, wave);
+      else if constexpr (v >= 0)
+        la.load(ta, la_at, oka, v, wave);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    // own loads of slab s + 2 landed, Fn read
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kVmem, 0));
+  };
+
+  static_for<0, kWords>([&](auto i) { load_scale(i, 0); });
+  take_scales();
+  char* const r1 = kPairs ? a0 : a1;
+  char* const r3 = kPairs ? a2 : a3;
+  issue_a(a0, a_first);
+  issue_b(b0, s0);
+  if constexpr (!kPairs) issue_a(r1, s0 + 1);
+  issue_b(b1, s0 + 1);
+  issue_a(a2, kPairs ? a_first + 1 : s0 + 2);
+  issue_b(b2, s0 + 2);
+  constexpr int kLast = kLoadsA + kLoadsB;   // loads after slab 1's
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kLast + kLoadsB + (kPairs ? 0 : kLoadsA), 15));   // slab 0 landed
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < kBM; ++i) fa[i] = ra.read(sa, kBM * wm + i);
-#pragma unroll
-    for (int j = 0; j < kBN; ++j) fb[j] = rb.read(sb, kBN * wn + j);
-    if constexpr (DT == kMX4) {
-      uint32_t xa[8], xb[8];
-      const int shift = 8 * int(s & 3);
-#pragma unroll
-      for (int i = 0; i < kBM; ++i) xa[i] = wa[i][(s >> 2) * 64] >> shift;
-#pragma unroll
-      for (int j = 0; j < kBN; ++j) xb[j] = wb[j][(s >> 2) * 64] >> shift;
-#pragma unroll
-      for (int i = 0; i < kBM; ++i)
-#pragma unroll
-        for (int j = 0; j < kBN; ++j)
-          acc[i][j] = mfma_mx4<0>(fb[j], fa[i], xb[j], xa[i], acc[i][j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBM; ++i)
-#pragma unroll
-        for (int j = 0; j < kBN; ++j) acc[i][j] = mfma<DT>(fb[j], fa[i], acc[i][j]);
-    }
-    __syncthreads();
+  for (int i = 0; i < kBM + kBN; ++i) read(a0, 0, b0, F0, i);
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kLast, 0));        // slab 1 landed, F0 read
+  for (int64_t s = s0; s < s1; s += 4) {
+    slab(std::integral_constant<int, 0>{}, s + 0, r1, b1, r3, b3, F0, F1);
+    slab(std::integral_constant<int, 1>{}, s + 1, a2, b2, a0, b0, F1, F0);
+    slab(std::integral_constant<int, 2>{}, s + 2, r3, b3, r1, b1, F0, F1);
+    slab(std::integral_constant<int, 3>{}, s + 3, a0, b0, a2, b2, F1, F0);
+    take_scales();
   }
+  // No load may still be writing LDS when the workgroup ends.
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+  settle();
+#pragma unroll
+  for (int i = 0; i < kBM; ++i)
+#pragma unroll
+    for (int j = 0; j < kBN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read from here on only
 
   const int64_t wave_m = m0 + 16 * kBM * wm + (lane & 15);
   if constexpr (EPI == kGated) {
@@ -449,7 +627,7 @@ __global__ __launch_bounds__(kTileWaves* kWave) void ffn_tile_kernel(TileArgs p,
 }
 
 template <int DT, int SRCA, int SRCB, int EPI, int TM, int TN>
-hipError_t launch_tile(const TileArgs& p, hipStream_t s) {
+hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
   const int64_t cols = EPI == kGated ? TN / 2 : TN;
   const int64_t MT = (p.M + TM - 1) / TM, NT = (p.N + cols - 1) / cols;
   const int64_t n = p.batch * MT * NT;
@@ -459,6 +637,15 @@ hipError_t launch_tile(const TileArgs& p, hipStream_t s) {
   hipLaunchKernelGGL(kern, dim3(unsigned(n), unsigned(p.splits > 1 ? p.splits : 1)),
                      dim3(kTileWaves * kWave), 0, s, p, n, MT, NT);
   return hipGetLastError();
+}
+
+template <int DT, int SRCA, int SRCB, int EPI>
+hipError_t launch_tile(const TileArgs& p, hipStream_t s) {
+  switch (p.tile) {
+    case kTile256: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 256>(p, s);
+    case kTile256x128: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 128>(p, s);
+    default: return launch_tile_of<DT, SRCA, SRCB, EPI, 128, 128>(p, s);
+  }
 }
 
 }  // namespace ffn

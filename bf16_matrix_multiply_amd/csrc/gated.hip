@@ -11,8 +11,8 @@ namespace bmm {
 
 hipError_t launch_gated(const TileArgs& a, int dtype, hipStream_t s) {
   using namespace ffn;
-  return dtype == kBF16 ? launch_tile<kBF16, kRows, kPacked2, kGated, 128, 128>(a, s)
-                        : launch_tile<kF16, kRows, kPacked2, kGated, 128, 128>(a, s);
+  return dtype == kBF16 ? launch_tile<kBF16, kRows, kPacked2, kGated>(a, s)
+                        : launch_tile<kF16, kRows, kPacked2, kGated>(a, s);
 }
 
 }  // namespace bmm

@@ -97,7 +97,7 @@ hipError_t join(const TileArgs& a, hipStream_t s) {
 
 template <int DT, int SRCA, int SRCB>
 hipError_t product(const TileArgs& a, hipStream_t s) {
-  hipError_t e = ffn::launch_tile<DT, SRCA, SRCB, ffn::kStore, 128, 128>(a, s);
+  hipError_t e = ffn::launch_tile<DT, SRCA, SRCB, ffn::kStore>(a, s);
   if (e == hipSuccess && a.splits > 1) e = join<DT>(a, s);
   return e;
 }
@@ -134,17 +134,20 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
                         : product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
 }
 
-// Splits of a product's summed axis (K values). Tiles of 128 x 128 run two to
-// a CU; a split keeps at least 16 slabs of 32 values, and 32 partial sums at
-// most are joined.
-int ffn_splits(int64_t batch, int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = batch * ((M + 127) / 128) * ((N + 127) / 128);
-  if (tiles == 0) return 1;
-  int64_t s = 512 / tiles;
-  const int64_t deep = K / 32 / 16;
-  if (s > deep) s = deep;
-  if (s > 32) s = 32;
-  return int(s < 1 ? 1 : s);
+TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
+  auto tiles = [&](int64_t tm, int64_t tn) {
+    return batch * ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+  };
+  TilePlan p{kTile128, 1};
+  if (tiles(256, 256) > 128) p.tile = kTile256;
+  else if (tiles(256, 128) > 128) p.tile = kTile256x128;
+  if (p.tile == kTile128 && may_split && batch * M * N > 0) {
+    int64_t s = 512 / tiles(128, 128);
+    if (s > slabs / 16) s = slabs / 16;
+    if (s > 32) s = 32;
+    p.splits = int(s < 1 ? 1 : s);
+  }
+  return p;
 }
 
 }  // namespace bmm

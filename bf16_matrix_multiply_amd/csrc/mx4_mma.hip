@@ -6,12 +6,12 @@ namespace bmm {
 
 hipError_t launch_mx4_mma(const TileArgs& a, hipStream_t s) {
   using namespace ffn;
-  return launch_tile<kMX4, kCodes, kCodes, kStore, 128, 128>(a, s);
+  return launch_tile<kMX4, kCodes, kCodes, kStore>(a, s);
 }
 
 hipError_t launch_mx4_gated(const TileArgs& a, hipStream_t s) {
   using namespace ffn;
-  return launch_tile<kMX4, kCodes, kCodes2, kGated, 128, 128>(a, s);
+  return launch_tile<kMX4, kCodes, kCodes2, kGated>(a, s);
 }
 
 }  // namespace bmm
