@@ -45,11 +45,20 @@
 //
 // Schedule: a ring of four stages. Slab s is multiplied from registers while
 // the wave reads the fragments of slab s + 1 from LDS into its second register
-// set and sends the loads of slab s + 3 into the stage that slab s - 1 has left;
+// set and sends the loads of slab s + 4 into the stage whose fragments it holds;
 // reads and loads are placed between the MFMAs, and one barrier a slab, after
 // its first two MFMAs, publishes the loads that every wave waited for at the end
 // of the slab before. The loop runs whole turns of the ring: slabs past the end
 // read as zeros.
+//
+// Measured on MI355X, 8192 x 4096 -> 8192 bf16: gated 755 us = 1456 TFLOP/s (the
+// library's plain 8192^3 product, as many operations, 670 us), of which 690 us
+// are the slab loops; 8192^3 with 4-bit operands 240 us = 4.6 PFLOP/s. Bound by
+// the matrix cores at the clock that the power limit leaves (bf16), and by the
+// LDS, whose reads and loads leave bubbles between the MFMAs of the one wave that
+// a SIMD has room for (4 bits: without them 169 us). Tried and slower: reads and
+// loads in bursts (820 -> 1000-1500 us), workgroups that go on to the next tile,
+// a copy of the loop for each wave with its reads and loads shifted.
 #pragma once
 
 #include <type_traits>
@@ -62,8 +71,8 @@ namespace ffn {
 enum Src : int { kRows, kTrans, kPacked2, kPackedT2, kCodes, kCodes2 };
 enum Epi : int { kStore, kGated };
 
-constexpr int kXcds = 8;
-constexpr int kGroupM = 8;
+constexpr uint32_t kXcds = 8;
+constexpr uint32_t kGroupM = 8;
 constexpr int kTileWaves = 4;
 constexpr int kBufferFlags = 0x00020000;           // raw, untyped buffer
 constexpr uint32_t kOutOfRange = 0x7fffffffu;      // an offset past every buffer's end
@@ -106,21 +115,24 @@ struct TileAt {
   int64_t b, mt, nt;
 };
 
-// Linear workgroup id -> work index, each XCD taking a contiguous run.
-__device__ __forceinline__ int64_t xcd_run(int64_t w, int64_t n) {
-  const int64_t q = n / kXcds, r = n % kXcds;
-  const int64_t xcd = w % kXcds, k = w / kXcds;
+// Linear workgroup id -> work index, each XCD taking a contiguous run. (All of
+// these fit 32 bits; 64-bit divisions took 1-2 us of every workgroup.)
+__device__ __forceinline__ uint32_t xcd_run(uint32_t w, uint32_t n) {
+  const uint32_t q = n / kXcds, r = n % kXcds;
+  const uint32_t xcd = w % kXcds, k = w / kXcds;
   return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
 // Linear tile index -> (batch, M tile, N tile), in bands of kGroupM M tiles.
-__device__ __forceinline__ TileAt tile_at(int64_t t, int64_t MT, int64_t NT) {
-  const int64_t per_batch = MT * NT;
-  const int64_t b = t / per_batch, u = t % per_batch;
-  const int64_t group = kGroupM * NT;
-  const int64_t first_m = (u / group) * kGroupM;
-  const int64_t gm = MT - first_m < kGroupM ? MT - first_m : kGroupM;
-  const int64_t v = u % group;
+__device__ __forceinline__ TileAt tile_at(uint32_t t, uint32_t MT, uint32_t NT, bool batched) {
+  uint32_t b = 0;
+  if (batched) {
+    b = t / (MT * NT);
+    t -= b * (MT * NT);
+  }
+  const uint32_t group = kGroupM * NT, first = t / group, first_m = first * kGroupM;
+  const uint32_t gm = MT - first_m < kGroupM ? MT - first_m : kGroupM;
+  const uint32_t v = t - first * group;
   return {b, first_m + v % gm, v / gm};
 }
 
@@ -319,6 +331,19 @@ struct Scales {
   }
 };
 
+// A sum from the accumulator registers, here and not earlier: with a branch for
+// each output type the compiler reads all 64 before it, more than fit.
+__device__ __forceinline__ f32x4 sum(f32x4 acc) {
+  f32x4 v;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(acc[e]));
+    v[e] = x;
+  }
+  return v;
+}
+
 // acc += b a^T over 32 values, in place. Written out, since the compiler gives
 // the result of its own form other registers than the sum it starts from; with
 // all 256 accumulator registers in use it then moved a third of them about in
@@ -363,23 +388,6 @@ __device__ __forceinline__ u32x4 join16(f32x4 v0, f32x4 v1) {
   return o;
 }
 
-// Writes blocks (v0, v1) at columns col0 .. col0 + 31 of the row at `row`
-// (null: the row does not exist), as out_type; n: columns that exist (a
-// multiple of 8).
-__device__ __forceinline__ void store_pair(void* row, int64_t col0, int64_t n, int out_type,
-                                           f32x4 v0, f32x4 v1, int g) {
-  if (out_type == BMM_ELEM_F32) {
-    const int64_t c = col0 + 4 * g;
-    float* at = static_cast<float*>(row) + c;
-    if (row && c < n) store16f(at, v0);
-    if (row && c + 16 < n) store16f(at + 16, v1);
-  } else {
-    const u32x4 o = out_type == BMM_ELEM_BF16 ? join16<kBF16>(v0, v1) : join16<kF16>(v0, v1);
-    const int64_t c = col0 + 16 * (g & 1) + 8 * (g >> 1);
-    if (row && c < n) *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(row) + c) = o;
-  }
-}
-
 template <int ACT>
 __device__ __forceinline__ f32x4 gate(f32x4 g, f32x4 u) {
   f32x4 h;
@@ -388,30 +396,18 @@ __device__ __forceinline__ f32x4 gate(f32x4 g, f32x4 u) {
   return h;
 }
 
-// Row pointer of an output of the given type, or null where the row is outside.
-__device__ __forceinline__ char* row_at(void* d, int64_t row, int64_t ld, int out_type, bool ok) {
-  const int64_t bytes = out_type == BMM_ELEM_F32 ? 4 : 2;
-  return ok ? static_cast<char*>(d) + row * ld * bytes : nullptr;
+// The output rows of a wave from d on, `left` of at most n: what lies past them
+// is not written.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(const void* d, int64_t row_bytes,
+                                                           int64_t left, int n) {
+  const int64_t rows = left < 0 ? 0 : left < n ? left : n;
+  return buffer(d, uint32_t(rows * row_bytes));   // ld <= 2^21: at most 2^30
 }
 
-template <int ACT>
-__device__ __forceinline__ void gated_blocks(const TileArgs& p, int64_t b, int64_t m, int64_t col0,
-                                             const f32x4 (&acc)[8], int blocks, int g) {
-  const bool ok = m < p.M;
-  const int64_t row = b * p.M + m;
-#pragma unroll
-  for (int j = 0; j < 8; j += 4) {
-    if (j >= blocks) break;
-    const int64_t c = col0 + 8 * j;
-    store_pair(row_at(p.d, row, p.ldd, p.out_type, ok), c, p.N, p.out_type,
-               gate<ACT>(acc[j], acc[j + 1]), gate<ACT>(acc[j + 2], acc[j + 3]), g);
-    if (p.d1) {
-      store_pair(row_at(p.d1, row, p.ldd, p.out_type, ok), c, p.N, p.out_type, acc[j], acc[j + 2], g);
-      store_pair(row_at(p.d2, row, p.ldd, p.out_type, ok), c, p.N, p.out_type, acc[j + 1],
-                 acc[j + 3], g);
-    }
-  }
-}
+// Outputs are touched once: non-temporal, so that they do not push the operands
+// out of the caches (gated with projections kept, 8192 x 4096 -> 8192: 819
+// against 843 us). Partial sums stay: the join reads them right after.
+constexpr int kNonTemporal = 2;
 
 // 256 rows: one workgroup a CU (a wave's 64 accumulators of 4 floats fill the
 // accumulator registers, so 128 x 128 of D come from 16 fragment reads);
@@ -419,7 +415,7 @@ __device__ __forceinline__ void gated_blocks(const TileArgs& p, int64_t b, int64
 template <int DT, int SRCA, int SRCB, int EPI, int TM, int TN>
 __global__ __launch_bounds__(kTileWaves* kWave)
 __attribute__((amdgpu_waves_per_eu(TM == 256 ? 1 : 2, TM == 256 ? 1 : 2)))
-void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
+void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   constexpr int kBM = TM / 32, kBN = TN / 32;   // 16-row and 16-column blocks a wave
   constexpr int kCols = EPI == kGated ? TN / 2 : TN;   // columns of D a tile
   static_assert((EPI == kGated) == two_sources(SRCB), "gated: two sources of B");
@@ -434,21 +430,32 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
-  const int64_t splits = p.splits > 1 ? p.splits : 1;
-  const int64_t work = xcd_run(int64_t(blockIdx.y) * n_tiles + blockIdx.x, n_tiles * splits);
-  const int64_t split = work / n_tiles;
-  const TileAt t = tile_at(work % n_tiles, MT, NT);
-  const int64_t m0 = t.mt * TM, n0 = t.nt * kCols;
+  const uint32_t splits = p.splits > 1 ? p.splits : 1, total = n_tiles * splits;
   constexpr int kValues = slab_values(SRCA);
   const int64_t slabs = (p.K + kValues - 1) / kValues;
-  // (a split starts at an even slab: rows come two slabs at a time)
-  const int64_t pairs = (slabs + 1) / 2, s0 = 2 * (split * pairs / splits);
-  const int64_t s1 = split + 1 < splits ? 2 * ((split + 1) * pairs / splits) : slabs;
 
   Loader<SRCA, TM> la;
   Loader<SRCB, TN> lb;
+  Scales ca, cb0, cb1;
+  uint32_t work = xcd_run(blockIdx.x, total), split = 0;
+  int64_t s0 = 0, s1 = slabs;   // the slabs to sum
+  if (splits > 1) {
+    split = work / n_tiles;
+    work -= split * n_tiles;
+    // (a split starts at an even slab: rows come two slabs at a time)
+    const uint32_t pairs = uint32_t((slabs + 1) / 2), q = pairs / splits, r = pairs % splits;
+    s0 = 2 * (int64_t(split) * q + (split < r ? split : r));
+    if (split + 1 < splits) s1 = s0 + 2 * (q + (split < r ? 1 : 0));
+  }
+  const TileAt t = tile_at(work, MT, NT, p.batch > 1);
+  const int64_t m0 = t.mt * TM, n0 = t.nt * kCols;
   la.init(p, p.a, nullptr, t.b * p.a_bs, p.lda, m0, p.M, s1, lane, wave);
   lb.init(p, p.b0, p.b1, t.b * p.b_bs, p.ldb, n0, p.N, s1, lane, wave);
+  if constexpr (DT == kMX4) {
+    ca.init(p.as, t.b * p.as_bs, p.K, m0, p.M);
+    cb0.init(p.bs0, t.b * p.bs_bs, p.K, n0, p.N);
+    if constexpr (EPI == kGated) cb1.init(p.bs1, t.b * p.bs_bs, p.K, n0, p.N);
+  }
   Reader<SRCA> ra;
   Reader<SRCB> rb;
   ra.init(lane);
@@ -468,7 +475,6 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
   };
 
   // 4-bit: this wave's scale words of four slabs, and of the next four
-  Scales ca, cb0, cb1;
   uint32_t xa[8], xb[8], ya[8], yb[8];
   constexpr int kWords = DT == kMX4 ? kBM + kBN : 0;
   auto load_scale = [&](auto word, int64_t q) {   // one of kWords
@@ -486,32 +492,15 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
       for (int j = 0; j < kBN; ++j) xb[j] = yb[j];
     }
   };
-  if constexpr (DT == kMX4) {
-    ca.init(p.as, t.b * p.as_bs, p.K, m0, p.M);
-    cb0.init(p.bs0, t.b * p.bs_bs, p.K, n0, p.N);
-    if constexpr (EPI == kGated) cb1.init(p.bs1, t.b * p.bs_bs, p.K, n0, p.N);
-  }
-
-  // Pinned to accumulator registers one by one: equal starting values would be
-  // merged, and the loop would then copy them.
   f32x4 acc[8][8];   // [16-row block][16-column block], kBM x kBN used
-#pragma unroll
-  for (int i = 0; i < kBM; ++i)
-#pragma unroll
-    for (int j = 0; j < kBN; ++j) {
-      f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      asm volatile("" : "+a"(v));
-      acc[i][j] = v;
-    }
-  settle();
-
   u32x4 F0[16], F1[16];   // one slab's fragments: B's kBN, then A's kBM
-  const int64_t a_first = kPairs ? s0 / 2 : s0;   // A's first round
   auto read = [&](const char* sa, int h, const char* sb, u32x4 (&F)[16], int i) {
     F[i] = i < kBN ? rb.read(sb, kBN * wn + i, 0) : ra.read(sa, kBM * wm + i - kBN, h);
   };
   // Slab s, the ring's turn-th: fragments Fc; reads slab s + 1 from (na, nb) to
-  // Fn; loads slab s + 3 to (ta, tb) (rows: slabs s + 3 and s + 4, in odd turns).
+  // Fn; loads slab s + 4 to this slab's own stage (ta, tb), whose fragments every
+  // wave has read (rows: slabs s + 3 and s + 4 to the stage of s - 1 and s, in
+  // odd turns).
   auto slab = [&](auto turn, int64_t s, const char* na, const char* nb, char* ta, char* tb,
                   const u32x4 (&Fc)[16], u32x4 (&Fn)[16]) {
     constexpr int SEL = decltype(turn)::value;
@@ -534,8 +523,8 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
     // sent in a burst they would wait for each other, and the MFMAs behind them.
     constexpr int kNowA = !kPairs || SEL % 2 == 1 ? kLoadsA : 0, kNow = kNowA + kLoadsB;
     bool oka, okb;
-    const auto la_at = la.round(kPairs ? (s - s0 + 3) / 2 + a_first : s + 3, oka);
-    const auto lb_at = lb.round(s + 3, okb);
+    const auto la_at = la.round(kPairs ? (s + 3) / 2 : s + 4, oka);   // (s0 is even)
+    const auto lb_at = lb.round(s + 4, okb);
     constexpr int kMfmas = kBM * kBN, kFrags = kBM + kBN;
     constexpr int kVmem = kNow + (SEL == 0 ? kWords : 0);
     static_for<2, kMfmas>([&](auto at) {
@@ -551,32 +540,48 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
         la.load(ta, la_at, oka, v, wave);
       __builtin_amdgcn_sched_barrier(0);
     });
-    // own loads of slab s + 2 landed, Fn read
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kVmem, 0));
+    // Fn read; own loads of slab s + 2 landed, which were sent in slab s - 2 (rows:
+    // an odd slab's, before that slab's loads of B, two or one slab ago)
+    constexpr int kBefore = kPairs ? kLoadsB : kLoadsA + kLoadsB;
+    constexpr int kOpen = kVmem + kBefore + (SEL == 1 && !kPairs ? kWords : 0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kOpen, 0));
   };
 
-  static_for<0, kWords>([&](auto i) { load_scale(i, 0); });
-  take_scales();
   char* const r1 = kPairs ? a0 : a1;
   char* const r3 = kPairs ? a2 : a3;
-  issue_a(a0, a_first);
+  static_for<0, kWords>([&](auto i) { load_scale(i, 0); });
+  issue_a(a0, kPairs ? s0 / 2 : s0);
   issue_b(b0, s0);
   if constexpr (!kPairs) issue_a(r1, s0 + 1);
   issue_b(b1, s0 + 1);
-  issue_a(a2, kPairs ? a_first + 1 : s0 + 2);
+  issue_a(a2, kPairs ? s0 / 2 + 1 : s0 + 2);
   issue_b(b2, s0 + 2);
-  constexpr int kLast = kLoadsA + kLoadsB;   // loads after slab 1's
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kLast + kLoadsB + (kPairs ? 0 : kLoadsA), 15));   // slab 0 landed
+  if constexpr (!kPairs) issue_a(r3, s0 + 3);
+  issue_b(b3, s0 + 3);
+  take_scales();
+  // Pinned to accumulator registers one by one: equal starting values would be
+  // merged, and the loop would then copy them.
+#pragma unroll
+  for (int i = 0; i < kBM; ++i)
+#pragma unroll
+    for (int j = 0; j < kBN; ++j) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      asm volatile("" : "+a"(v));
+      acc[i][j] = v;
+    }
+  settle();
+  // slabs 0 and 1 landed (after them: rows, one round of A and two of B)
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm((kPairs ? 1 : 2) * kLoadsA + 2 * kLoadsB, 15));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
   for (int i = 0; i < kBM + kBN; ++i) read(a0, 0, b0, F0, i);
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kLast, 0));        // slab 1 landed, F0 read
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
   for (int64_t s = s0; s < s1; s += 4) {
-    slab(std::integral_constant<int, 0>{}, s + 0, r1, b1, r3, b3, F0, F1);
-    slab(std::integral_constant<int, 1>{}, s + 1, a2, b2, a0, b0, F1, F0);
-    slab(std::integral_constant<int, 2>{}, s + 2, r3, b3, r1, b1, F0, F1);
-    slab(std::integral_constant<int, 3>{}, s + 3, a0, b0, a2, b2, F1, F0);
+    slab(std::integral_constant<int, 0>{}, s + 0, r1, b1, a0, b0, F0, F1);
+    slab(std::integral_constant<int, 1>{}, s + 1, a2, b2, r1, b1, F1, F0);
+    slab(std::integral_constant<int, 2>{}, s + 2, r3, b3, a2, b2, F0, F1);
+    slab(std::integral_constant<int, 3>{}, s + 3, a0, b0, r3, b3, F1, F0);
     take_scales();
   }
   // No load may still be writing LDS when the workgroup ends.
@@ -586,42 +591,109 @@ void ffn_tile_kernel(TileArgs p, int64_t n_tiles, int64_t MT, int64_t NT) {
   for (int i = 0; i < kBM; ++i)
 #pragma unroll
     for (int j = 0; j < kBN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read from here on only
-
-  const int64_t wave_m = m0 + 16 * kBM * wm + (lane & 15);
+  const int64_t row = m0 + 16 * kBM * wm, col = n0 + (EPI == kGated ? 8 : 16) * kBN * wn;
+  constexpr int kPairsN = EPI == kGated ? kBN / 4 : kBN / 2;   // 32-column pieces
+  // float32 results: partial sums, and the 4-bit product's where it is asked for
+  const bool wide = EPI == kStore && (DT == kMX4 ? p.out_type == BMM_ELEM_F32 : splits > 1);
+  u32x4 out[8][2];
   if constexpr (EPI == kGated) {
-    const int64_t col0 = n0 + 8 * kBN * wn;
-    auto rows = [&](auto a) {
+    auto gate_all = [&](auto type, auto a) {
+      constexpr int T = decltype(type)::value, A = decltype(a)::value;
 #pragma unroll
       for (int i = 0; i < kBM; ++i)
-        gated_blocks<decltype(a)::value>(p, t.b, wave_m + 16 * i, col0, acc[i], kBN, g);
+#pragma unroll
+        for (int j = 0; j < kPairsN; ++j)
+          out[i][j] = join16<T>(gate<A>(acc[i][4 * j], acc[i][4 * j + 1]),
+                                gate<A>(acc[i][4 * j + 2], acc[i][4 * j + 3]));
+    };
+    auto gate_type = [&](auto a) {
+      if constexpr (DT != kMX4) gate_all(std::integral_constant<int, DT>{}, a);
+      else if (p.out_type == BMM_ELEM_BF16) gate_all(std::integral_constant<int, kBF16>{}, a);
+      else gate_all(std::integral_constant<int, kF16>{}, a);
     };
     switch (p.act) {
-      case BMM_ACT_SILU: rows(std::integral_constant<int, BMM_ACT_SILU>{}); break;
-      case BMM_ACT_GELU: rows(std::integral_constant<int, BMM_ACT_GELU>{}); break;
-      case BMM_ACT_GELU_TANH: rows(std::integral_constant<int, BMM_ACT_GELU_TANH>{}); break;
-      default: rows(std::integral_constant<int, BMM_ACT_RELU>{});
+      case BMM_ACT_SILU: gate_type(std::integral_constant<int, BMM_ACT_SILU>{}); break;
+      case BMM_ACT_GELU: gate_type(std::integral_constant<int, BMM_ACT_GELU>{}); break;
+      case BMM_ACT_GELU_TANH: gate_type(std::integral_constant<int, BMM_ACT_GELU_TANH>{}); break;
+      default: gate_type(std::integral_constant<int, BMM_ACT_RELU>{});
+    }
+  }
+
+  // Offsets of this lane's columns in the first 16 rows; those outside are past
+  // every buffer's end.
+  const int64_t ld = EPI == kStore && splits > 1 ? p.N : p.ldd;
+  const uint32_t row_bytes = uint32_t(ld) * (wide ? 4 : 2), step = 16 * row_bytes;
+  uint32_t at[8];
+  auto offsets = [&]() {
+#pragma unroll
+    for (int j = 0; j < (wide ? kBN : kPairsN); ++j) {
+      const int c = wide ? 16 * j + 4 * g : 32 * j + 16 * (g & 1) + 8 * (g >> 1);
+      at[j] = col + c < p.N ? (lane & 15) * row_bytes + (wide ? 4 : 2) * c : kOutOfRange;
+    }
+  };
+  if constexpr (EPI == kGated) {
+    auto store = [&](void* d, auto value) {
+      const auto to = out_rows(static_cast<uint16_t*>(d) + (t.b * p.M + row) * ld + col,
+                               row_bytes, p.M - row, 16 * kBM);
+      offsets();
+#pragma unroll
+      for (int i = 0; i < kBM; ++i)
+#pragma unroll
+        for (int j = 0; j < kPairsN; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(value(i, j), to, at[j] + i * step, 0, kNonTemporal);
+    };
+    store(p.d, [&](int i, int j) { return out[i][j]; });
+    if constexpr (DT != kMX4) {
+      if (p.d1) {
+        store(p.d1, [&](int i, int j) { return join16<DT>(acc[i][4 * j], acc[i][4 * j + 2]); });
+        store(p.d2, [&](int i, int j) { return join16<DT>(acc[i][4 * j + 1], acc[i][4 * j + 3]); });
+      }
     }
   } else {
-    const int64_t col0 = n0 + 16 * kBN * wn;
-#pragma unroll
-    for (int i = 0; i < kBM; ++i) {
-      const int64_t m = wave_m + 16 * i;
-      char* row;
-      int out_type = p.out_type;
-      if (splits > 1) {
-        row = m < p.M ? reinterpret_cast<char*>(p.part + split * p.part_floats +
-                                                (t.b * p.M + m) * p.N)
-                      : nullptr;
-        out_type = BMM_ELEM_F32;
-      } else if (m < p.rows0) {
-        row = row_at(p.d, t.b * p.rows0 + m, p.ldd, out_type, true);
-      } else {
-        const int64_t r = m - p.row1;
-        row = row_at(p.d1, t.b * p.rows0 + r, p.ldd, out_type, r >= 0 && r < p.rows0);
+    // Rows below rows0 go to d, those from row1 (a multiple of 16) on to d1.
+    const int size = wide ? 4 : 2;
+    const bool parts = splits > 1;
+    const char* d = parts ? reinterpret_cast<char*>(p.part + split * p.part_floats)
+                          : static_cast<char*>(p.d);
+    const int64_t rows = parts ? p.M : p.rows0;
+    const auto to = out_rows(d + ((t.b * rows + row) * ld + col) * size, row_bytes,
+                             rows - row, 16 * kBM);
+    auto to1 = to;
+    int second = kBM;   // first block of 16 rows that goes to d1
+    if constexpr (SRCA == kTrans) {
+      if (!parts && row + 16 * kBM > p.row1) {
+        second = row < p.row1 ? int(p.row1 - row) / 16 : 0;
+        to1 = out_rows(static_cast<char*>(p.d1) +
+                           ((t.b * rows + row - p.row1) * ld + col) * size,
+                       row_bytes, p.row1 + rows - row, 16 * kBM);
       }
+    }
+    offsets();
+    auto store = [&](int i, int j, u32x4 v, auto nt) {
+      __builtin_amdgcn_raw_buffer_store_b128(v, SRCA == kTrans && i >= second ? to1 : to,
+                                             at[j] + i * step, 0, decltype(nt)::value);
+    };
+    auto store16 = [&](auto type) {
 #pragma unroll
-      for (int j = 0; j < kBN; j += 2)
-        store_pair(row, col0 + 16 * j, p.N, out_type, acc[i][j], acc[i][j + 1], g);
+      for (int i = 0; i < kBM; ++i)
+#pragma unroll
+        for (int j = 0; j < kPairsN; ++j)
+          store(i, j, join16<decltype(type)::value>(sum(acc[i][2 * j]), sum(acc[i][2 * j + 1])),
+                std::integral_constant<int, kNonTemporal>{});
+    };
+    auto store32 = [&](auto nt) {
+#pragma unroll
+      for (int i = 0; i < kBM; ++i)
+#pragma unroll
+        for (int j = 0; j < kBN; ++j) store(i, j, __builtin_bit_cast(u32x4, acc[i][j]), nt);
+    };
+    if constexpr (DT != kMX4) {
+      if (wide) store32(std::integral_constant<int, 0>{});
+      else store16(std::integral_constant<int, DT>{});
+    } else {
+      if (wide) store32(std::integral_constant<int, kNonTemporal>{});
+      else if (p.out_type == BMM_ELEM_BF16) store16(std::integral_constant<int, kBF16>{});
+      else store16(std::integral_constant<int, kF16>{});
     }
   }
 }
@@ -631,11 +703,13 @@ hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
   const int64_t cols = EPI == kGated ? TN / 2 : TN;
   const int64_t MT = (p.M + TM - 1) / TM, NT = (p.N + cols - 1) / cols;
   const int64_t n = p.batch * MT * NT;
-  if (n > 0x7fffffff) return hipErrorInvalidConfiguration;
+  const int64_t splits = p.splits > 1 ? p.splits : 1;
   if (n == 0) return hipSuccess;
+  if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37)
+    return hipErrorInvalidConfiguration;
   auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, TM, TN>;
-  hipLaunchKernelGGL(kern, dim3(unsigned(n), unsigned(p.splits > 1 ? p.splits : 1)),
-                     dim3(kTileWaves * kWave), 0, s, p, n, MT, NT);
+  hipLaunchKernelGGL(kern, dim3(unsigned(n * splits)), dim3(kTileWaves * kWave), 0, s, p,
+                     uint32_t(n), uint32_t(MT), uint32_t(NT));
   return hipGetLastError();
 }
 

@@ -205,7 +205,8 @@ Status check_mx4_product(const void* D, const uint8_t* A, const uint8_t* As, con
   if (ab < 0 || asb < 0 || bb < 0 || bsb < 0)
     return failw(what, BMM_EINVAL, "extent too large (K < 2^22)");
   if (ld < N) return failw(what, BMM_EINVAL, "ld (%lld) < %lld columns", ld, N);
-  if (ld > kMaxExtent || mul_capped({batch, M, ld, size}) < 0)
+  if (ld > kMaxLd) return failw(what, BMM_EINVAL, "ld (%lld) is at most 2^21", ld);
+  if (mul_capped({batch, M, ld, size}) < 0)
     return failw(what, BMM_EINVAL, "too large");
   if (ld % 8) return failw(what, BMM_EALIGN, "ld (%lld) must be a multiple of 8 elements", ld);
   if (batch == 0 || M == 0 || N == 0) return Status{};

@@ -536,7 +536,8 @@ int bmm_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales, i
  * bmm_mx4_mma — D = A * B^T over 4-bit operands.
  *
  * D  (batch, M, ld_d) of elem_type (BMM_ELEM_F32, _F16 or _BF16), written in
- *    the first N columns; ld_d >= N, a multiple of 8, 16-byte aligned.
+ *    the first N columns; ld_d >= N, a multiple of 8, at most 2^21; 16-byte
+ *    aligned.
  * A  4-bit operand of M rows, B of N rows, both of K values; N a multiple of 8.
  * Sums are float32, rounded once. K = 0 gives zeros; zero batch, M or N is a
  * no-op.
