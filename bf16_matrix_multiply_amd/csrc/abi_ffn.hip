@@ -87,7 +87,7 @@ int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const ui
     a.ldd = d.ld_h;
     a.a_bs = d.M * d.ld_x;
     a.b_bs = d.F * d.K;
-    a.tile = bmm::plan_tiles(d.batch, d.M, 2 * d.F, d.K / 32, false).tile;
+    a.tile = bmm::plan_forward(d.batch, d.M, 2 * d.F, d.K / 32);
     return hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
                       "gated launch");
   });
@@ -231,7 +231,7 @@ int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const 
     a.bs_bs = bmm::mx4_scales_bytes(1, N, K);
     a.out_type = elem_type;
     a.splits = 1;
-    a.tile = bmm::plan_tiles(batch, M, N, K / 128, false).tile;
+    a.tile = bmm::plan_forward(batch, M, N, K / 128);
     return hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
   });
 }
@@ -266,7 +266,7 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
     a.act = act;
     a.out_type = elem_type;
     a.splits = 1;
-    a.tile = bmm::plan_tiles(batch, M, 2 * F, K / 128, false).tile;
+    a.tile = bmm::plan_forward(batch, M, 2 * F, K / 128);
     return hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
                       "mx4_gated launch");
   });

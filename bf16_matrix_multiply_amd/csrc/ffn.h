@@ -15,8 +15,9 @@ namespace bmm {
 // with a scale for every 32 K values.
 enum : int { kMX4 = 2 };
 
-// Rows x columns of a product's tile (gated: columns of both weights).
-enum TileSize : int { kTile128, kTile256x128, kTile256 };
+// How a product is made: by tiles of so many rows x columns (gated: columns of
+// both weights), or by the kernel for few rows (ffn_skinny.h).
+enum TileSize : int { kTile128, kTile256x128, kTile256, kSkinny };
 
 // One product D = A * B^T on MFMA tiles. Which fields count depends on how
 // the operands lie in memory and on the epilogue (ffn_tile.h).
@@ -71,6 +72,8 @@ struct TilePlan {
   int tile, splits;
 };
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split);
+// The same for a product that has the kernel for few rows and no splits.
+int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs);
 
 // ---- activations ----
 // exp is the hardware's 2^x (1 ulp) of x log2(e); the product's rounding makes

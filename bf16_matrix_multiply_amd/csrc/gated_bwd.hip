@@ -134,20 +134,54 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
                         : product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
 }
 
+// The plan that a simple model finds fastest. A tile of each size takes so long a
+// slab and so long besides (its first loads and its results), in nanoseconds, when
+// the chip is full (256 workgroups; 128 x 128: 512) and when at most half of it is
+// used. The tiles run in rounds; of 128 x 128 tiles, two on a CU, the last round
+// starts while the one before it ends. Split sums are written and read once, 8
+// bytes at 5 TB/s, and joined by one more launch. Measured on MI355X (us; model in
+// parentheses): the weight gradients of 32773 x 512 -> 1024 by 256 x 256 tiles and
+// 16 splits 63 (82), by 128 x 128 tiles without splits 258 (291); dX of 8192 x
+// 1024 -> 1024 by 256 x 128 tiles 33 (34), 128 x 128 33 (34), 256 x 256 45 (45);
+// gated 1500 x 2048 -> 5464 by 128 x 128 tiles 71 (69), 256 x 128 82 (95), 256 x
+// 256 93 (99).
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
-  auto tiles = [&](int64_t tm, int64_t tn) {
-    return batch * ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+  struct Size {
+    int64_t tm, tn, places, full, half, besides;
   };
-  TilePlan p{kTile128, 1};
-  if (tiles(256, 256) > 128) p.tile = kTile256;
-  else if (tiles(256, 128) > 128) p.tile = kTile256x128;
-  if (p.tile == kTile128 && may_split && batch * M * N > 0) {
-    int64_t s = 512 / tiles(128, 128);
-    if (s > slabs / 16) s = slabs / 16;
-    if (s > 32) s = 32;
-    p.splits = int(s < 1 ? 1 : s);
+  static constexpr Size kSizes[] = {{128, 128, 512, 470, 280, 4000},
+                                    {256, 128, 256, 450, 350, 5000},
+                                    {256, 256, 256, 730, 600, 7000}};
+  static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+  TilePlan best{kTile128, 1};
+  double least = 0;
+  for (int size = 0; size < 3; ++size) {
+    const Size& z = kSizes[size];
+    const double tiles = double(batch) * ((M + z.tm - 1) / z.tm) * ((N + z.tn - 1) / z.tn);
+    for (int splits : kSplits) {
+      if (splits > 1 && (!may_split || slabs / splits < 8)) break;
+      const double n = tiles * splits, rounds = n < 1e15 ? double(int64_t(n) / z.places) : 1e12;
+      const double rest = n - rounds * z.places, per = double((slabs + splits - 1) / splits);
+      double cost = rounds * (per * z.full + z.besides);
+      if (rest > 0 && size == 0 && rounds > 0)
+        cost *= n / (rounds * z.places);
+      else if (rest > 0)
+        cost += per * (2 * rest <= z.places ? z.half : z.full) + z.besides;
+      if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * batch * double(M) * N;
+      if ((size == 0 && splits == 1) || cost < least) {
+        least = cost;
+        best = {size, splits};
+      }
+    }
   }
-  return p;
+  return best;
+}
+
+// Few rows: the weights are read once for up to 64 rows. Gated 4096 -> 8192 bf16:
+// 64 rows 43-46 us against 50 by 128 x 128 tiles, 96 rows 67 against 51.
+int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs) {
+  if (M <= 64 && batch <= 65535) return kSkinny;
+  return plan_tiles(batch, M, N, slabs, false).tile;
 }
 
 }  // namespace bmm
