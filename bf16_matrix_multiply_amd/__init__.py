@@ -482,9 +482,25 @@ def _act_code(act: str, fn: str) -> int:
         raise ValueError(f"{fn}: unknown activation {act!r}; expected one of {sorted(ACTS)}") from None
 
 
+# One token's calls last about as long on the GPU as their marshalling does, so
+# the common case of each check below comes first and costs a few attribute
+# reads; the slow path names the fault.
+
+def _raw_stream() -> int:
+    """The current device's current torch stream, as the C ABI takes it."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
 def _rows_ld(t: torch.Tensor, name: str, fn: str) -> int:
     """Elements between the rows of a (rows, cols) or (batch, rows, cols) matrix
     with unit innermost stride and batches rows * ld apart."""
+    stride = t.stride()
+    if len(stride) == 2 and stride[1] == 1 and t.shape[0] > 1 and t.shape[1] > 1:
+        return stride[0]
     if t.dim() not in (2, 3):
         raise ValueError(f"{fn}: {name} must be (rows, cols) or (batch, rows, cols)")
     rows, cols = t.shape[-2:]
@@ -498,25 +514,29 @@ def _rows_ld(t: torch.Tensor, name: str, fn: str) -> int:
     return ld
 
 
-def _out(t, shape, dtype, device, name, fn):
+def _out(t, shape, dtype, like, fn):
+    """The output and the elements between its rows."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {tuple(shape)}")
-    return t
+        return like.new_empty(shape, dtype=dtype), shape[-1]
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{fn}: out must be a {dtype} tensor of shape {tuple(shape)}")
+    return t, _rows_ld(t, "out", fn)
 
 
 def _gated_weights(Wg, Wu, batch, K, fn) -> int:
     """F of two packed weights (batch, F/8, K/16, 8, 8)."""
+    shape = Wg.shape
+    if len(shape) == 5 and shape == (batch, shape[1], K >> 4, 8, 8) and Wu.shape == shape \
+            and K & 15 == 0 and Wg.element_size() == 4 and Wu.element_size() == 4 \
+            and Wg.is_contiguous() and Wu.is_contiguous():
+        return 8 * shape[1]
     for w, name in ((Wg, "Wg"), (Wu, "Wu")):
         if w.dim() != 5 or w.shape[3:] != (8, 8) or w.element_size() != 4 or not w.is_contiguous():
             raise ValueError(f"{fn}: {name} must be contiguous packed words (batch, F/8, K/16, 8, 8) "
                              "(pack_operand with atom_rows 8)")
     if Wg.shape != Wu.shape:
         raise ValueError(f"{fn}: Wg and Wu differ in shape")
-    if Wg.shape[0] != batch or 16 * Wg.shape[2] != K:
-        raise ValueError(f"{fn}: X and the weights disagree on batch or K")
-    return 8 * Wg.shape[1]
+    raise ValueError(f"{fn}: X and the weights disagree on batch or K")
 
 
 def _half_matrix(t, name, fn):
@@ -539,20 +559,18 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
     _require_cuda(X, Wg, Wu, out)
     dt = _half_matrix(X, "X", "gated")
     ld_x = _rows_ld(X, "X", "gated")
-    batch = X.shape[0] if X.dim() == 3 else 1
-    M, K = X.shape[-2:]
+    *lead, M, K = X.shape
+    batch = lead[0] if lead else 1
     F = _gated_weights(Wg, Wu, batch, K, "gated")
-    shape = (*X.shape[:-1], F)
-    H = _out(out, shape, X.dtype, X.device, "out", "gated")
-    ld_h = _rows_ld(H, "out", "gated")
+    H, ld_h = _out(out, (*lead, M, F), X.dtype, X, "gated")
     G = U = None
     if save:
         if ld_h != F and H.numel():
             raise ValueError("gated: with save, out must be contiguous")
-        G, U = torch.empty_like(H), torch.empty_like(H)
+        G, U = X.new_empty((*lead, M, F)), X.new_empty((*lead, M, F))
     d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
-    _check(lib().bmm_gated(_ptr(H), _ptr(G), _ptr(U), _ptr(X), _ptr(Wg), _ptr(Wu),
-                           ctypes.byref(d), _stream(X)))
+    _check(lib().bmm_gated(_addr(H), _addr(G), _addr(U), _addr(X), _addr(Wg), _addr(Wu),
+                           ctypes.byref(d), _raw_stream()))
     return (H, G, U) if save else H
 
 
@@ -580,29 +598,30 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.
     _require_cuda(dH, G, U, X, Wg, Wu, workspace)
     dt = _half_matrix(X, "X", fn)
     ld_x = _rows_ld(X, "X", fn)
-    batch = X.shape[0] if X.dim() == 3 else 1
-    M, K = X.shape[-2:]
+    *lead, M, K = X.shape
+    batch = lead[0] if lead else 1
     F = _gated_weights(Wg, Wu, batch, K, fn)
     ld_h = _rows_ld(dH, "dH", fn)
+    shape, stride, dtype = (*lead, M, F), dH.stride(), X.dtype
     for t, name in ((dH, "dH"), (G, "G"), (U, "U")):
-        if tuple(t.shape) != (*X.shape[:-1], F) or t.dtype != X.dtype:
-            raise ValueError(f"{fn}: {name} must be a {X.dtype} tensor of shape {(*X.shape[:-1], F)}")
-        if _rows_ld(t, name, fn) != ld_h:
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {shape}")
+        if t.stride() != stride and _rows_ld(t, name, fn) != ld_h:
             raise ValueError(f"{fn}: dH, G and U must have the same row stride")
     d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
     need = _check(lib().bmm_gated_backward_workspace_bytes(ctypes.byref(d)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = X.new_empty(need, dtype=torch.uint8)
     elif not workspace.is_contiguous():
         raise ValueError(f"{fn}: workspace must be contiguous")
-    dX = torch.empty(X.shape, dtype=X.dtype, device=X.device) if need_dx else None
+    dX = X.new_empty((*lead, M, K)) if need_dx else None
     dWg = dWu = None
     if need_dw:
-        dWg = torch.empty((*X.shape[:-2], F, K), dtype=X.dtype, device=X.device)
-        dWu = torch.empty_like(dWg)
-    _check(lib().bmm_gated_backward(_ptr(dX), _ptr(dWg), _ptr(dWu), _ptr(dH), _ptr(G), _ptr(U),
-                                    _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(d), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(X)))
+        dWg = X.new_empty((*lead, F, K))
+        dWu = X.new_empty((*lead, F, K))
+    _check(lib().bmm_gated_backward(_addr(dX), _addr(dWg), _addr(dWu), _addr(dH), _addr(G), _addr(U),
+                                    _addr(X), _addr(Wg), _addr(Wu), ctypes.byref(d), _addr(workspace),
+                                    workspace.numel() * workspace.element_size(), _raw_stream()))
     return dX, dWg, dWu
 
 
@@ -627,47 +646,55 @@ def _mx4_shapes(batch, rows, K):
     return (batch, r16, -(-K // 128), 4, 16, 16), (batch, r16, -(-K // 512), 4, 16, 4)
 
 
-def _mx4_check(op: Mx4Operand, name, fn):
-    want = _mx4_shapes(op.batch, op.rows, op.K)
-    for t, shape, part in ((op.codes, want[0], "codes"), (op.scales, want[1], "scales")):
-        if tuple(t.shape) != shape or t.dtype != torch.uint8 or not t.is_contiguous():
+def _mx4_check(op: Mx4Operand, name, fn) -> int:
+    """The operand's batch count."""
+    codes, scales, rows, K, batched = op
+    batch = codes.shape[0]
+    want = _mx4_shapes(batch, rows, K)
+    if codes.shape == want[0] and scales.shape == want[1] and codes.dtype == scales.dtype == \
+            torch.uint8 and codes.is_contiguous() and scales.is_contiguous() and \
+            codes.is_cuda and scales.is_cuda and (batched or batch == 1):
+        return batch
+    for t, shape, part in ((codes, want[0], "codes"), (scales, want[1], "scales")):
+        if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
             raise ValueError(f"{fn}: {name}.{part} must be a contiguous uint8 tensor of shape {shape}")
-    if op.batch != 1 and not op.batched:
-        raise ValueError(f"{fn}: {name} has {op.batch} batches but is not batched")
-    _require_cuda(op.codes, op.scales)
+    if batch != 1 and not batched:
+        raise ValueError(f"{fn}: {name} has {batch} batches but is not batched")
+    _require_cuda(codes, scales)
 
 
 def mx4_quantize(X: torch.Tensor) -> Mx4Operand:
     """(rows, K) or (batch, rows, K) float32, float16 or bfloat16 to a 4-bit
     operand (bmm_mx4_quantize): blocks of 32 along K, one power-of-two scale
     each. K is a multiple of 32; rows may be any multiple of 8 elements apart."""
+    fn = "mx4_quantize"
     _require_cuda(X)
     if X.dtype not in _ELEM_DTYPES:
-        raise ValueError(f"mx4_quantize: X must be float32, float16 or bfloat16, got {X.dtype}")
-    ld = _rows_ld(X, "X", "mx4_quantize")
-    batch = X.shape[0] if X.dim() == 3 else 1
-    rows, K = X.shape[-2:]
+        raise ValueError(f"{fn}: X must be float32, float16 or bfloat16, got {X.dtype}")
+    ld = _rows_ld(X, "X", fn)
+    *lead, rows, K = X.shape
+    batch = lead[0] if lead else 1
     cs, ss = _mx4_shapes(batch, rows, K)
-    codes = torch.empty(cs, dtype=torch.uint8, device=X.device)
-    scales = torch.empty(ss, dtype=torch.uint8, device=X.device)
-    _check(lib().bmm_mx4_quantize(_ptr(codes), _ptr(scales), _ptr(X), batch, rows, K, ld,
-                                  _ELEM_DTYPES[X.dtype], _stream(X)))
-    return Mx4Operand(codes, scales, rows, K, X.dim() == 3)
+    codes = X.new_empty(cs, dtype=torch.uint8)
+    scales = X.new_empty(ss, dtype=torch.uint8)
+    _check(lib().bmm_mx4_quantize(codes.data_ptr(), scales.data_ptr(), X.data_ptr(), batch, rows, K,
+                                  ld, _ELEM_DTYPES[X.dtype], _raw_stream()))
+    return Mx4Operand(codes, scales, rows, K, bool(lead))
 
 
 def mx4_dequantize(A: Mx4Operand, dtype: torch.dtype = torch.float32,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """The (rows, K) or (batch, rows, K) values of a 4-bit operand in ``dtype``
     (bmm_mx4_dequantize)."""
-    _mx4_check(A, "A", "mx4_dequantize")
+    fn = "mx4_dequantize"
+    batch = _mx4_check(A, "A", fn)
     _require_cuda(out)
     if dtype not in _ELEM_DTYPES:
-        raise ValueError(f"mx4_dequantize: dtype must be float32, float16 or bfloat16, got {dtype}")
-    shape = (A.batch, A.rows, A.K) if A.batched else (A.rows, A.K)
-    out = _out(out, shape, dtype, A.codes.device, "out", "mx4_dequantize")
-    ld = _rows_ld(out, "out", "mx4_dequantize")
-    _check(lib().bmm_mx4_dequantize(_ptr(out), _ptr(A.codes), _ptr(A.scales), A.batch, A.rows, A.K,
-                                    ld, _ELEM_DTYPES[dtype], _stream(A.codes)))
+        raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
+    codes, scales, rows, K, batched = A
+    out, ld = _out(out, (batch, rows, K) if batched else (rows, K), dtype, codes, fn)
+    _check(lib().bmm_mx4_dequantize(out.data_ptr(), codes.data_ptr(), scales.data_ptr(), batch, rows,
+                                    K, ld, _ELEM_DTYPES[dtype], _raw_stream()))
     return out
 
 
@@ -676,19 +703,20 @@ def mx4_mma(A: Mx4Operand, B: Mx4Operand, dtype: torch.dtype = torch.float32,
     """D = A * B^T over 4-bit operands (bmm_mx4_mma): row-major (M, N) or (batch,
     M, N) in ``dtype`` (float32, float16 or bfloat16). B's rows are a multiple
     of 8."""
-    _mx4_check(A, "A", "mx4_mma")
-    _mx4_check(B, "B", "mx4_mma")
+    fn = "mx4_mma"
+    batch = _mx4_check(A, "A", fn)
+    batch_b = _mx4_check(B, "B", fn)
     _require_cuda(out)
     if dtype not in _ELEM_DTYPES:
-        raise ValueError(f"mx4_mma: dtype must be float32, float16 or bfloat16, got {dtype}")
-    if A.batch != B.batch or A.K != B.K:
-        raise ValueError("mx4_mma: A and B disagree on batch or K")
-    shape = (A.batch, A.rows, B.rows) if A.batched else (A.rows, B.rows)
-    out = _out(out, shape, dtype, A.codes.device, "out", "mx4_mma")
-    ld = _rows_ld(out, "out", "mx4_mma")
-    _check(lib().bmm_mx4_mma(_ptr(out), _ptr(A.codes), _ptr(A.scales), _ptr(B.codes),
-                             _ptr(B.scales), A.batch, A.rows, B.rows, A.K, ld,
-                             _ELEM_DTYPES[dtype], _stream(A.codes)))
+        raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
+    a, a_scales, M, K, batched = A
+    b, b_scales, N, K_b, _ = B
+    if batch != batch_b or K != K_b:
+        raise ValueError(f"{fn}: A and B disagree on batch or K")
+    out, ld = _out(out, (batch, M, N) if batched else (M, N), dtype, a, fn)
+    _check(lib().bmm_mx4_mma(out.data_ptr(), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+                             b_scales.data_ptr(), batch, M, N, K, ld, _ELEM_DTYPES[dtype],
+                             _raw_stream()))
     return out
 
 
@@ -698,20 +726,22 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     """H = act(X Wg^T) * (X Wu^T) over 4-bit operands (bmm_mx4_gated): row-major
     (M, F) or (batch, M, F) in ``dtype`` (float16 or bfloat16). The weights' F
     rows are a multiple of 8."""
-    code = _act_code(act, "mx4_gated")
-    for op, name in ((X, "X"), (Wg, "Wg"), (Wu, "Wu")):
-        _mx4_check(op, name, "mx4_gated")
+    fn = "mx4_gated"
+    code = _act_code(act, fn)
+    batch = _mx4_check(X, "X", fn)
+    batch_g, batch_u = _mx4_check(Wg, "Wg", fn), _mx4_check(Wu, "Wu", fn)
     _require_cuda(out)
     if dtype not in _HALF_DTYPES:
-        raise ValueError(f"mx4_gated: dtype must be float16 or bfloat16, got {dtype}")
-    if Wg.rows != Wu.rows or Wg.K != Wu.K or Wg.batch != Wu.batch:
-        raise ValueError("mx4_gated: Wg and Wu differ in shape")
-    if X.batch != Wg.batch or X.K != Wg.K:
-        raise ValueError("mx4_gated: X and the weights disagree on batch or K")
-    shape = (X.batch, X.rows, Wg.rows) if X.batched else (X.rows, Wg.rows)
-    out = _out(out, shape, dtype, X.codes.device, "out", "mx4_gated")
-    ld = _rows_ld(out, "out", "mx4_gated")
-    _check(lib().bmm_mx4_gated(_ptr(out), _ptr(X.codes), _ptr(X.scales), _ptr(Wg.codes),
-                               _ptr(Wg.scales), _ptr(Wu.codes), _ptr(Wu.scales), X.batch, X.rows,
-                               Wg.rows, X.K, ld, code, _ELEM_DTYPES[dtype], _stream(X.codes)))
+        raise ValueError(f"{fn}: dtype must be float16 or bfloat16, got {dtype}")
+    x, x_scales, M, K, batched = X
+    g, g_scales, F, K_g, _ = Wg
+    u, u_scales, F_u, K_u, _ = Wu
+    if F != F_u or K_g != K_u or batch_g != batch_u:
+        raise ValueError(f"{fn}: Wg and Wu differ in shape")
+    if batch != batch_g or K != K_g:
+        raise ValueError(f"{fn}: X and the weights disagree on batch or K")
+    out, ld = _out(out, (batch, M, F) if batched else (M, F), dtype, x, fn)
+    _check(lib().bmm_mx4_gated(out.data_ptr(), x.data_ptr(), x_scales.data_ptr(), g.data_ptr(),
+                               g_scales.data_ptr(), u.data_ptr(), u_scales.data_ptr(), batch, M, F,
+                               K, ld, code, _ELEM_DTYPES[dtype], _raw_stream()))
     return out
