@@ -134,24 +134,26 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
                         : product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
 }
 
-// The plan that a simple model finds fastest. A tile of each size takes so long a
-// slab and so long besides (its first loads and its results), in nanoseconds, when
-// the chip is full (256 workgroups; 128 x 128: 512) and when at most half of it is
-// used. The tiles run in rounds; of 128 x 128 tiles, two on a CU, the last round
-// starts while the one before it ends. Split sums are written and read once, 8
-// bytes at 5 TB/s, and joined by one more launch. Measured on MI355X (us; model in
-// parentheses): the weight gradients of 32773 x 512 -> 1024 by 256 x 256 tiles and
-// 16 splits 63 (82), by 128 x 128 tiles without splits 258 (291); dX of 8192 x
-// 1024 -> 1024 by 256 x 128 tiles 33 (34), 128 x 128 33 (34), 256 x 256 45 (45);
-// gated 1500 x 2048 -> 5464 by 128 x 128 tiles 71 (69), 256 x 128 82 (95), 256 x
-// 256 93 (99).
+// The plan that a simple model finds fastest. A tile of each size takes so many
+// nanoseconds a slab and so many besides (its first loads and its results) on a
+// full chip (256 workgroups; 128 x 128: 512). The tiles run in rounds; one that
+// fills a share f of the chip takes a + (1 - a) f of a full one, with another a for
+// the first round than for a later one, which starts while the one before it ends.
+// Split sums are written and read once, 8 bytes at 5 TB/s, and joined by one more
+// launch. The constants are a fit to 51 products measured on MI355X (16-bit and
+// 4-bit, 128 to 32773 rows): 7% off in the mean, and within 3% of the fastest size
+// in all but two. For example gated 1500 x 2048 -> 5464 by 128 x 128 tiles 71 us,
+// 256 x 128 82, 256 x 256 93, but 4095 rows 168, 171 and 148; the weight gradients
+// of 32773 x 512 -> 1024 by 128 x 128 tiles 258 us, with 8 splits 79, by 256 x 256
+// tiles and 16 splits 63.
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
   struct Size {
-    int64_t tm, tn, places, full, half, besides;
+    int64_t tm, tn, places;
+    double slab, besides, first, later;
   };
-  static constexpr Size kSizes[] = {{128, 128, 512, 470, 280, 4000},
-                                    {256, 128, 256, 450, 350, 5000},
-                                    {256, 256, 256, 730, 600, 7000}};
+  static constexpr Size kSizes[] = {{128, 128, 512, 475, 3300, .45, .16},
+                                    {256, 128, 256, 435, 5000, .71, .50},
+                                    {256, 256, 256, 715, 8200, .70, .63}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   TilePlan best{kTile128, 1};
   double least = 0;
@@ -160,13 +162,11 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
     const double tiles = double(batch) * ((M + z.tm - 1) / z.tm) * ((N + z.tn - 1) / z.tn);
     for (int splits : kSplits) {
       if (splits > 1 && (!may_split || slabs / splits < 8)) break;
-      const double n = tiles * splits, rounds = n < 1e15 ? double(int64_t(n) / z.places) : 1e12;
-      const double rest = n - rounds * z.places, per = double((slabs + splits - 1) / splits);
-      double cost = rounds * (per * z.full + z.besides);
-      if (rest > 0 && size == 0 && rounds > 0)
-        cost *= n / (rounds * z.places);
-      else if (rest > 0)
-        cost += per * (2 * rest <= z.places ? z.half : z.full) + z.besides;
+      const double tile = double((slabs + splits - 1) / splits) * z.slab + z.besides;
+      const double fill = tiles * splits / z.places, rounds = fill < 1e12 ? double(int64_t(fill)) : fill;
+      const double a = rounds > 0 ? z.later : z.first;
+      double cost = rounds * tile;
+      if (fill > rounds) cost += tile * (a + (1 - a) * (fill - rounds));
       if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * batch * double(M) * N;
       if ((size == 0 && splits == 1) || cost < least) {
         least = cost;
