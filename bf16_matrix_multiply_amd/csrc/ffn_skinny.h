@@ -2,18 +2,18 @@
 // decoded): bound by reading the weights once.
 //
 // A workgroup makes MR groups of 16 rows by NB blocks of 16 columns (gated: NB / 2
-// blocks of both weights, alternating), its W waves each a contiguous range of
-// the summed axis. A wave streams its part of the weights from memory to
-// registers, four steps (32 16-bit or 128 4-bit values each) at a time: 4 NB
-// loads of 1 KB in flight, and with 16 waves on a CU more than the memory needs
-// to keep busy (8 TB/s x 1.5 us = 47 KB a CU). X is small, read by every
-// workgroup and cached. The partial sums meet in LDS, the upper half of the
-// waves first, then the lower half in order: the same result on every run.
+// blocks of both weights, alternating); its W waves share the summed axis. A wave
+// streams its part of the weights from memory to registers, a round of four steps
+// (32 16-bit or 128 4-bit values each) at a time: 4 NB loads of 1 KB in flight, and
+// with 16 waves on a CU more than the memory needs to keep busy (8 TB/s x 1.5 us =
+// 47 KB a CU). X is small, read by every workgroup and cached. The partial sums
+// meet in LDS, the upper half of the waves first, then the lower half in order: the
+// same result on every run.
 //
-// Measured on MI355X, weights cold: one token through 2 x 8192 x 4096 bf16 24 us =
-// 5.6 TB/s, through 16384 x 16384 4-bit weights 29 us = 4.8 TB/s; a long read
-// reaches 6.5. Eight steps at a time, 16 waves, or loads that stay in the caches
-// changed it by -1 to +2 us.
+// Measured on MI355X, weights cold: one token through 2 x 8192 x 4096 bf16 22.4 us =
+// 6.0 TB/s, through 16384 x 16384 4-bit weights 24 us = 5.8 TB/s; a long read
+// reaches 6.5. Eight steps at a time, 16 waves, a second set of registers for the
+// next round, or loads that stay in the caches changed it by -1 to +4 us.
 //
 // Fragments as in ffn_tile.h: lane l supplies row l % 16 and the 16 bytes of
 // summed chunk l / 16, and holds D[m = l % 16][n = 4 (l / 16) .. + 3]. Loads go
@@ -37,6 +37,12 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
   constexpr int kValues = k4 ? 128 : 32;              // summed values a step
   constexpr int kBytesB = k4 ? 1024 : 512;            // of a lane's row, from step to step
   constexpr int kBytesA = k4 ? 1024 : 64;
+  // Whether the waves take the rounds in turns, so that together they read on in
+  // each row, or each a range of its own. Measured, in turns against ranges: 16-bit
+  // weights 22.4 / 23.8 us (one token, 4096 -> 8192), 21.4 / 31.6 (8192 -> 4096);
+  // 4-bit product 24.0 / 29.4 (16384 x 16384), but for 32 rows 22.1 / 17.6 (4096 x
+  // 16384) and 30.1 / 32.4 (16384 x 16384); 4-bit gated 27.2 / 25.0 (8192 -> 16384).
+  constexpr bool kTurns = !k4 || (EPI == kStore && MR == 1);
   __shared__ __attribute__((aligned(16))) f32x4 red[W / 2][MR][NB][kWave];
 
   const int lane = threadIdx.x & (kWave - 1);
@@ -85,8 +91,8 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
     for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   const int64_t rounds = (p.K + kSteps * kValues - 1) / (kSteps * kValues);
-  const int64_t q0 = wave * rounds / W, q1 = (wave + 1) * rounds / W;
-  for (int64_t q = q0; q < q1; ++q) {
+  const int64_t q0 = kTurns ? wave : wave * rounds / W, q1 = kTurns ? rounds : (wave + 1) * rounds / W;
+  for (int64_t q = q0; q < q1; q += kTurns ? W : 1) {
     u32x4 fb[kSteps][4], fa[kSteps][4];
     uint32_t xa[4], xb[4];
     const auto rb0 = buffer(bases_b[0] + q * (kSteps * kBytesB));

@@ -72,7 +72,7 @@ enum Src : int { kRows, kTrans, kPacked2, kPackedT2, kCodes, kCodes2 };
 enum Epi : int { kStore, kGated };
 
 constexpr uint32_t kXcds = 8;
-constexpr uint32_t kGroupM = 8;
+constexpr uint32_t kGroupM = 4;
 constexpr int kTileWaves = 4;
 constexpr int kBufferFlags = 0x00020000;           // raw, untyped buffer
 constexpr uint32_t kOutOfRange = 0x7fffffffu;      // an offset past every buffer's end
