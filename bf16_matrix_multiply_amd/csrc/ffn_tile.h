@@ -466,12 +466,14 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     const auto at = la.round(k, ok);
 #pragma unroll
     for (int r = 0; r < kLoadsA; ++r) la.load(stage, at, ok, r, wave);
+    __builtin_amdgcn_sched_barrier(0);   // the waits below count the loads in this order
   };
   auto issue_b = [&](char* stage, int64_t k) {
     bool ok;
     const auto at = lb.round(k, ok);
 #pragma unroll
     for (int r = 0; r < kLoadsB; ++r) lb.load(stage, at, ok, r, wave);
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   // 4-bit: this wave's scale words of four slabs, and of the next four
@@ -550,6 +552,7 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   char* const r1 = kPairs ? a0 : a1;
   char* const r3 = kPairs ? a2 : a3;
   static_for<0, kWords>([&](auto i) { load_scale(i, 0); });
+  __builtin_amdgcn_sched_barrier(0);
   issue_a(a0, kPairs ? s0 / 2 : s0);
   issue_b(b0, s0);
   if constexpr (!kPairs) issue_a(r1, s0 + 1);
