@@ -70,6 +70,7 @@ hipError_t launch_mx4_gated(const TileArgs& a, hipStream_t s);
 // How a product of M rows, N columns (gated: of both weights) and so many slabs is cut.
 struct TilePlan {
   int tile, splits;
+  double ns;   // what the model expects
 };
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split);
 // The same for a product that has the kernel for few rows and no splits.

@@ -155,8 +155,7 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
                                     {256, 128, 256, 435, 5000, .71, .50},
                                     {256, 256, 256, 715, 8200, .70, .63}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
-  TilePlan best{kTile128, 1};
-  double least = 0;
+  TilePlan best{kTile128, 1, 0};
   for (int size = 0; size < 3; ++size) {
     const Size& z = kSizes[size];
     const double tiles = double(batch) * ((M + z.tm - 1) / z.tm) * ((N + z.tn - 1) / z.tn);
@@ -168,10 +167,7 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
       double cost = rounds * tile;
       if (fill > rounds) cost += tile * (a + (1 - a) * (fill - rounds));
       if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * batch * double(M) * N;
-      if ((size == 0 && splits == 1) || cost < least) {
-        least = cost;
-        best = {size, splits};
-      }
+      if ((size == 0 && splits == 1) || cost < best.ns) best = {size, splits, cost};
     }
   }
   return best;

@@ -51,6 +51,8 @@ BACK = [  # (batch, M, F, K, pad, dtype, act)
     (1, 3001, 3080, 2064, 8, BF, "silu"), (1, 6000, 1032, 2064, 0, HF, "gelu"),
     (1, 12000, 1032, 1040, 0, BF, "gelu_tanh"), (2, 1500, 1032, 784, 0, HF, "relu"),
     (1, 20011, 264, 272, 24, BF, "silu"), (1, 700, 2056, 2048, 0, BF, "gelu"),
+    # dX in two launches: whole rounds of large tiles, and the rows left
+    (1, 8229, 1032, 2048, 8, HF, "silu"), (1, 4111, 1032, 4096, 0, BF, "gelu_tanh"),
 ]
 
 
