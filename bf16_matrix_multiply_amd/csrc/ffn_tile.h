@@ -257,46 +257,46 @@ struct Loader {
   }
 };
 
-// This lane's 16 bytes of fragment f (rows 16 f .. of the tile) in a stage;
+// This lane's 16 bytes of the wave's fragment f (16 rows of the tile) in a stage;
 // rows: of slab h of the stage's two.
 template <int SRC>
 struct Reader {
-  int at[4];      // byte offset of the lane within a piece; rows: by h;
-                  // transposed: of the four exchanges of chunk pairs
+  int at[4];      // byte offset of the lane in the wave's first fragment; rows: by h;
+                  // transposed: in the first four
   int at4[4];     // transposed: four summed rows on
 
-  __device__ __forceinline__ void init(int lane) {
+  // first: the wave's first fragment.
+  __device__ __forceinline__ void init(int lane, int first) {
     const int i = lane & 15, g = lane >> 4;
     if constexpr (SRC == kRows) {
-      at[0] = 128 * i + 16 * (g ^ rows_swizzle(i));
+      at[0] = 2048 * first + 128 * i + 16 * (g ^ rows_swizzle(i));
       at[1] = at[0] ^ 64;
-    } else if constexpr (SRC == kTrans) {
+    } else if constexpr (SRC == kTrans || SRC == kPackedT2) {
       const int k = 8 * g + (i >> 2);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        at[b] = 128 * k + 8 * (i & 3) + 32 * (b ^ trans_swizzle(k));
-        at4[b] = at[b] + 512;
+        const int f = first + b;
+        if constexpr (SRC == kTrans) {
+          at[b] = 4096 * (f >> 2) + 128 * k + 8 * (i & 3) + 32 * ((f & 3) ^ trans_swizzle(k));
+          at4[b] = at[b] + 512;
+        } else {
+          at[b] = 4096 * (f >> 2) + 256 * (f & 3) + 1024 * g + ((8 * i) ^ (128 * (g & 1)));
+          at4[b] = at[b] ^ 128;
+        }
+        // kept apart: the compiler follows an address only a few steps back to
+        // its stage, and waits for every load in flight where it cannot
+        asm volatile("" : "+v"(at4[b]));
       }
-    } else if constexpr (SRC == kPackedT2) {
-      at[0] = 1024 * g + ((8 * i) ^ (128 * (g & 1)));
-      at4[0] = at[0] ^ 128;
     } else if constexpr (SRC == kPacked2) {
-      at[0] = 512 * (i >> 3) + 256 * (g >> 1) + 32 * (i & 7) + 16 * (g & 1);
+      at[0] = 1024 * first + 512 * (i >> 3) + 256 * (g >> 1) + 32 * (i & 7) + 16 * (g & 1);
     } else {
-      at[0] = 16 * lane;
-    }
-    if constexpr (SRC == kTrans || SRC == kPackedT2) {
-      // kept apart: the compiler follows an address only a few steps back to
-      // its stage, and waits for every load in flight where it cannot
-#pragma unroll
-      for (int b = 0; b < (SRC == kTrans ? 4 : 1); ++b) asm volatile("" : "+v"(at4[b]));
+      at[0] = 1024 * first + 16 * lane;
     }
   }
 
   __device__ __forceinline__ u32x4 read(const char* stage, int f, int h) const {
     if constexpr (SRC == kTrans || SRC == kPackedT2) {
-      const int b = SRC == kTrans ? f & 3 : 0;
-      const int block = 4096 * (f >> 2) + (SRC == kPackedT2 ? 256 * (f & 3) : 0);
+      const int block = 4096 * (f >> 2), b = f & 3;
       const u32x2 lo = __builtin_bit_cast(
           u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(stage + (block + at[b]))));
       const u32x2 hi = __builtin_bit_cast(
@@ -390,6 +390,11 @@ __device__ __forceinline__ u32x4 join16(f32x4 v0, f32x4 v1) {
   return o;
 }
 
+template <int DT>
+__device__ __forceinline__ u32x2 pack4(f32x4 v) {
+  return u32x2{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+}
+
 template <int ACT>
 __device__ __forceinline__ f32x4 gate(f32x4 g, f32x4 u) {
   f32x4 h;
@@ -460,8 +465,8 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   }
   Reader<SRCA> ra;
   Reader<SRCB> rb;
-  ra.init(lane);
-  rb.init(lane);
+  ra.init(lane, kBM * wm);
+  rb.init(lane, kBN * wn);
   constexpr int kLoadsA = Loader<SRCA, TM>::kLoads, kLoadsB = Loader<SRCB, TN>::kLoads;
   auto issue_a = [&](char* stage, int64_t k) {
     bool ok;
@@ -499,7 +504,7 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   f32x4 acc[8][8];   // [16-row block][16-column block], kBM x kBN used
   u32x4 F0[16], F1[16];   // one slab's fragments: B's kBN, then A's kBM
   auto read = [&](const char* sa, int h, const char* sb, u32x4 (&F)[16], int i) {
-    F[i] = i < kBN ? rb.read(sb, kBN * wn + i, 0) : ra.read(sa, kBM * wm + i - kBN, h);
+    F[i] = i < kBN ? rb.read(sb, i, 0) : ra.read(sa, i - kBN, h);
   };
   // Slab s, the ring's turn-th: fragments Fc; reads slab s + 1 from (na, nb) to
   // Fn; loads slab s + 4 to this slab's own stage (ta, tb), whose fragments every
@@ -600,7 +605,10 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   constexpr int kPairsN = EPI == kGated ? kBN / 4 : kBN / 2;   // 32-column pieces
   // float32 results: partial sums, and the 4-bit product's where it is asked for
   const bool wide = EPI == kStore && (DT == kMX4 ? p.out_type == BMM_ELEM_F32 : splits > 1);
+  // (192 columns: 48 of H a wave, the last 16 by themselves)
+  constexpr bool kLast = EPI == kGated && kBN % 4 != 0;
   u32x4 out[8][2];
+  u32x2 last[8];
   if constexpr (EPI == kGated) {
     auto gate_all = [&](auto type, auto a) {
       constexpr int T = decltype(type)::value, A = decltype(a)::value;
@@ -610,6 +618,10 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
         for (int j = 0; j < kPairsN; ++j)
           out[i][j] = join16<T>(gate<A>(acc[i][4 * j], acc[i][4 * j + 1]),
                                 gate<A>(acc[i][4 * j + 2], acc[i][4 * j + 3]));
+      if constexpr (kLast) {
+#pragma unroll
+        for (int i = 0; i < kBM; ++i) last[i] = pack4<T>(gate<A>(acc[i][kBN - 2], acc[i][kBN - 1]));
+      }
     };
     auto gate_type = [&](auto a) {
       if constexpr (DT != kMX4) gate_all(std::integral_constant<int, DT>{}, a);
@@ -637,7 +649,7 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     }
   };
   if constexpr (EPI == kGated) {
-    auto store = [&](void* d, auto value) {
+    auto store = [&](void* d, auto value, auto last_value) {
       const auto to = out_rows(static_cast<uint16_t*>(d) + (t.b * p.M + row) * ld + col,
                                row_bytes, p.M - row, 16 * kBM);
       offsets();
@@ -646,12 +658,21 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
           __builtin_amdgcn_raw_buffer_store_b128(value(i, j), to, at[j] + i * step, 0, kNonTemporal);
+      if constexpr (kLast) {
+        const int c = 32 * kPairsN + 4 * g;
+        const uint32_t at_last = col + c < p.N ? (lane & 15) * row_bytes + 2 * c : kOutOfRange;
+#pragma unroll
+        for (int i = 0; i < kBM; ++i)
+          __builtin_amdgcn_raw_buffer_store_b64(last_value(i), to, at_last + i * step, 0, kNonTemporal);
+      }
     };
-    store(p.d, [&](int i, int j) { return out[i][j]; });
+    store(p.d, [&](int i, int j) { return out[i][j]; }, [&](int i) { return last[i]; });
     if constexpr (DT != kMX4) {
       if (p.d1) {
-        store(p.d1, [&](int i, int j) { return join16<DT>(acc[i][4 * j], acc[i][4 * j + 2]); });
-        store(p.d2, [&](int i, int j) { return join16<DT>(acc[i][4 * j + 1], acc[i][4 * j + 3]); });
+        store(p.d1, [&](int i, int j) { return join16<DT>(acc[i][4 * j], acc[i][4 * j + 2]); },
+              [&](int i) { return pack4<DT>(acc[i][kBN - 2]); });
+        store(p.d2, [&](int i, int j) { return join16<DT>(acc[i][4 * j + 1], acc[i][4 * j + 3]); },
+              [&](int i) { return pack4<DT>(acc[i][kBN - 1]); });
       }
     }
   } else {
@@ -723,6 +744,7 @@ hipError_t launch_tile(const TileArgs& p, hipStream_t s) {
   switch (p.tile) {
     case kTile256: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 256>(p, s);
     case kTile256x128: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 128>(p, s);
+    case kTile256x192: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 192>(p, s);
     default: return launch_tile_of<DT, SRCA, SRCB, EPI, 128, 128>(p, s);
   }
 }

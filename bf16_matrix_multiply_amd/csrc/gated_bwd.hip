@@ -140,23 +140,24 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
 // fills a share f of the chip takes a + (1 - a) f of a full one, with another a for
 // the first round than for a later one, which starts while the one before it ends.
 // Split sums are written and read once, 8 bytes at 5 TB/s, and joined by one more
-// launch. The constants are a fit to 51 products measured on MI355X (16-bit and
-// 4-bit, 128 to 32773 rows): 7% off in the mean, and within 3% of the fastest size
-// in all but two. For example gated 1500 x 2048 -> 5464 by 128 x 128 tiles 71 us,
-// 256 x 128 82, 256 x 256 93, but 4095 rows 168, 171 and 148; the weight gradients
-// of 32773 x 512 -> 1024 by 128 x 128 tiles 258 us, with 8 splits 79, by 256 x 256
-// tiles and 16 splits 63.
+// launch. The constants are a fit to 60 products measured on MI355X (16-bit and
+// 4-bit, 200 to 32773 rows): 7% off in the mean, and within 3% of the fastest size
+// in all but two. For example gated K = 2048 -> 5464 by tiles of 128 x 128, 256 x
+// 128, 256 x 192 and 256 x 256: 777 rows 45.5, 52.3, 39.0 and 43.2 us, 1500 rows
+// 70, 83, 77 and 92, 4095 rows 163, 172, 164 and 148; the weight gradients of 32773
+// x 512 -> 1024 by 128 x 128 tiles 258 us, by 256 x 128 tiles and 8 splits 72.
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
   struct Size {
     int64_t tm, tn, places;
     double slab, besides, first, later;
   };
-  static constexpr Size kSizes[] = {{128, 128, 512, 475, 3300, .45, .16},
-                                    {256, 128, 256, 435, 5000, .71, .50},
-                                    {256, 256, 256, 715, 8200, .70, .63}};
+  static constexpr Size kSizes[] = {{128, 128, 512, 475, 3600, .45, .08},
+                                    {256, 128, 256, 418, 4900, .74, .60},
+                                    {256, 192, 256, 525, 7900, .77, .87},
+                                    {256, 256, 256, 672, 9300, .77, .56}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   TilePlan best{kTile128, 1, 0};
-  for (int size = 0; size < 3; ++size) {
+  for (int size = 0; size < 4; ++size) {
     const Size& z = kSizes[size];
     const double tiles = double(batch) * ((M + z.tm - 1) / z.tm) * ((N + z.tn - 1) / z.tn);
     for (int splits : kSplits) {

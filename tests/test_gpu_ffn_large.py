@@ -29,6 +29,7 @@ GATED = [  # (batch, M, F, K, pad, dtype, act)
     (2, 1030, 4104, 2064, 8, BF, "gelu"), (1, 2051, 4104, 1040, 0, HF, "relu"),
     (1, 17, 1160, 2064, 0, BF, "silu"), (1, 49, 2056, 1040, 24, HF, "gelu"),
     (3, 64, 520, 272, 0, BF, "gelu_tanh"), (1, 2, 4104, 4112, 0, BF, "relu"),
+    (1, 2000, 1544, 4112, 0, BF, "gelu"),
 ]
 
 
@@ -53,6 +54,8 @@ BACK = [  # (batch, M, F, K, pad, dtype, act)
     (1, 20011, 264, 272, 24, BF, "silu"), (1, 700, 2056, 2048, 0, BF, "gelu"),
     # dX in two launches: whole rounds of large tiles, and the rows left
     (1, 8229, 1032, 2048, 8, HF, "silu"), (1, 4111, 1032, 4096, 0, BF, "gelu_tanh"),
+    # tiles of 192 columns, with and without splits
+    (1, 5000, 1408, 2048, 0, BF, "relu"), (1, 3000, 4104, 1536, 0, HF, "silu"),
 ]
 
 
@@ -85,7 +88,7 @@ def operand(gen, rows, K, batch, spread=6):
 
 PRODUCTS = [  # (batch, M, N, K)
     (0, 1503, 8200, 4128), (0, 2051, 4104, 1056), (2, 1030, 2056, 544), (0, 40, 4104, 4128),
-    (0, 64, 520, 160), (2, 23, 1160, 2080), (0, 13, 4104, 8224),
+    (0, 64, 520, 160), (2, 23, 1160, 2080), (0, 13, 4104, 8224), (0, 1003, 10920, 4128),
 ]
 
 
@@ -105,6 +108,7 @@ def test_mx4_product(i):
 MX4_GATED = [  # (batch, M, F, K, dtype, act)
     (0, 1003, 8200, 2080, BF, "silu"), (0, 4095, 2056, 1056, HF, "gelu_tanh"),
     (2, 530, 1032, 288, BF, "gelu"), (0, 50, 2056, 4128, HF, "silu"), (0, 7, 4104, 4128, BF, "relu"),
+    (0, 1003, 5464, 4128, BF, "gelu"),
 ]
 
 
