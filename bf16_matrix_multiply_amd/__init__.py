@@ -486,9 +486,13 @@ def _act_code(act: str, fn: str) -> int:
 # the common case of each check below comes first and costs a few attribute
 # reads; the slow path names the fault.
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream() -> int:
     """The current device's current torch stream, as the C ABI takes it."""
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _current_stream(_current_device())
 
 
 def _addr(t: torch.Tensor | None):
@@ -499,8 +503,12 @@ def _rows_ld(t: torch.Tensor, name: str, fn: str) -> int:
     """Elements between the rows of a (rows, cols) or (batch, rows, cols) matrix
     with unit innermost stride and batches rows * ld apart."""
     stride = t.stride()
-    if len(stride) == 2 and stride[1] == 1 and t.shape[0] > 1 and t.shape[1] > 1:
-        return stride[0]
+    if len(stride) == 2 and stride[1] == 1:
+        rows, cols = t.shape
+        if rows <= 1:
+            return (cols + 7) >> 3 << 3
+        if cols > 1:
+            return stride[0]
     if t.dim() not in (2, 3):
         raise ValueError(f"{fn}: {name} must be (rows, cols) or (batch, rows, cols)")
     rows, cols = t.shape[-2:]
@@ -556,7 +564,8 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
     the same type. Returns H (..., M, F) in X's type, and with ``save`` (H, G,
     U), the projections that gated_backward takes. ``act`` is one of ACTS."""
     code = _act_code(act, "gated")
-    _require_cuda(X, Wg, Wu, out)
+    if not (X.is_cuda and Wg.is_cuda and Wu.is_cuda and out is None):
+        _require_cuda(X, Wg, Wu, out)
     dt = _half_matrix(X, "X", "gated")
     ld_x = _rows_ld(X, "X", "gated")
     *lead, M, K = X.shape
@@ -569,8 +578,11 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
             raise ValueError("gated: with save, out must be contiguous")
         G, U = X.new_empty((*lead, M, F)), X.new_empty((*lead, M, F))
     d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
-    _check(lib().bmm_gated(_addr(H), _addr(G), _addr(U), _addr(X), _addr(Wg), _addr(Wu),
-                           ctypes.byref(d), _raw_stream()))
+    rc = (_lib or lib()).bmm_gated(H.data_ptr(), _addr(G), _addr(U), X.data_ptr(), Wg.data_ptr(),
+                                   Wu.data_ptr(), ctypes.byref(d),
+                                   _current_stream(_current_device()))
+    if rc < 0:
+        _check(rc)
     return (H, G, U) if save else H
 
 
@@ -642,8 +654,8 @@ class Mx4Operand(typing.NamedTuple):
 
 
 def _mx4_shapes(batch, rows, K):
-    r16 = -(-rows // 16)
-    return (batch, r16, -(-K // 128), 4, 16, 16), (batch, r16, -(-K // 512), 4, 16, 4)
+    r16 = (rows + 15) >> 4
+    return (batch, r16, (K + 127) >> 7, 4, 16, 16), (batch, r16, (K + 511) >> 9, 4, 16, 4)
 
 
 def _mx4_check(op: Mx4Operand, name, fn) -> int:
@@ -668,17 +680,21 @@ def mx4_quantize(X: torch.Tensor) -> Mx4Operand:
     operand (bmm_mx4_quantize): blocks of 32 along K, one power-of-two scale
     each. K is a multiple of 32; rows may be any multiple of 8 elements apart."""
     fn = "mx4_quantize"
-    _require_cuda(X)
-    if X.dtype not in _ELEM_DTYPES:
+    if not X.is_cuda:
+        _require_cuda(X)
+    elem = _ELEM_DTYPES.get(X.dtype)
+    if elem is None:
         raise ValueError(f"{fn}: X must be float32, float16 or bfloat16, got {X.dtype}")
     ld = _rows_ld(X, "X", fn)
     *lead, rows, K = X.shape
     batch = lead[0] if lead else 1
     cs, ss = _mx4_shapes(batch, rows, K)
     codes = X.new_empty(cs, dtype=torch.uint8)
-    scales = X.new_empty(ss, dtype=torch.uint8)
-    _check(lib().bmm_mx4_quantize(codes.data_ptr(), scales.data_ptr(), X.data_ptr(), batch, rows, K,
-                                  ld, _ELEM_DTYPES[X.dtype], _raw_stream()))
+    scales = codes.new_empty(ss)
+    rc = (_lib or lib()).bmm_mx4_quantize(codes.data_ptr(), scales.data_ptr(), X.data_ptr(), batch,
+                                          rows, K, ld, elem, _current_stream(_current_device()))
+    if rc < 0:
+        _check(rc)
     return Mx4Operand(codes, scales, rows, K, bool(lead))
 
 
@@ -688,13 +704,18 @@ def mx4_dequantize(A: Mx4Operand, dtype: torch.dtype = torch.float32,
     (bmm_mx4_dequantize)."""
     fn = "mx4_dequantize"
     batch = _mx4_check(A, "A", fn)
-    _require_cuda(out)
-    if dtype not in _ELEM_DTYPES:
+    if out is not None:
+        _require_cuda(out)
+    elem = _ELEM_DTYPES.get(dtype)
+    if elem is None:
         raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
     codes, scales, rows, K, batched = A
     out, ld = _out(out, (batch, rows, K) if batched else (rows, K), dtype, codes, fn)
-    _check(lib().bmm_mx4_dequantize(out.data_ptr(), codes.data_ptr(), scales.data_ptr(), batch, rows,
-                                    K, ld, _ELEM_DTYPES[dtype], _raw_stream()))
+    rc = (_lib or lib()).bmm_mx4_dequantize(out.data_ptr(), codes.data_ptr(), scales.data_ptr(),
+                                            batch, rows, K, ld, elem,
+                                            _current_stream(_current_device()))
+    if rc < 0:
+        _check(rc)
     return out
 
 
@@ -706,17 +727,21 @@ def mx4_mma(A: Mx4Operand, B: Mx4Operand, dtype: torch.dtype = torch.float32,
     fn = "mx4_mma"
     batch = _mx4_check(A, "A", fn)
     batch_b = _mx4_check(B, "B", fn)
-    _require_cuda(out)
-    if dtype not in _ELEM_DTYPES:
+    if out is not None:
+        _require_cuda(out)
+    elem = _ELEM_DTYPES.get(dtype)
+    if elem is None:
         raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
     a, a_scales, M, K, batched = A
     b, b_scales, N, K_b, _ = B
     if batch != batch_b or K != K_b:
         raise ValueError(f"{fn}: A and B disagree on batch or K")
     out, ld = _out(out, (batch, M, N) if batched else (M, N), dtype, a, fn)
-    _check(lib().bmm_mx4_mma(out.data_ptr(), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
-                             b_scales.data_ptr(), batch, M, N, K, ld, _ELEM_DTYPES[dtype],
-                             _raw_stream()))
+    rc = (_lib or lib()).bmm_mx4_mma(out.data_ptr(), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
+                                     b_scales.data_ptr(), batch, M, N, K, ld, elem,
+                                     _current_stream(_current_device()))
+    if rc < 0:
+        _check(rc)
     return out
 
 
@@ -730,7 +755,8 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     code = _act_code(act, fn)
     batch = _mx4_check(X, "X", fn)
     batch_g, batch_u = _mx4_check(Wg, "Wg", fn), _mx4_check(Wu, "Wu", fn)
-    _require_cuda(out)
+    if out is not None:
+        _require_cuda(out)
     if dtype not in _HALF_DTYPES:
         raise ValueError(f"{fn}: dtype must be float16 or bfloat16, got {dtype}")
     x, x_scales, M, K, batched = X
@@ -741,7 +767,10 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     if batch != batch_g or K != K_g:
         raise ValueError(f"{fn}: X and the weights disagree on batch or K")
     out, ld = _out(out, (batch, M, F) if batched else (M, F), dtype, x, fn)
-    _check(lib().bmm_mx4_gated(out.data_ptr(), x.data_ptr(), x_scales.data_ptr(), g.data_ptr(),
-                               g_scales.data_ptr(), u.data_ptr(), u_scales.data_ptr(), batch, M, F,
-                               K, ld, code, _ELEM_DTYPES[dtype], _raw_stream()))
+    rc = (_lib or lib()).bmm_mx4_gated(out.data_ptr(), x.data_ptr(), x_scales.data_ptr(),
+                                       g.data_ptr(), g_scales.data_ptr(), u.data_ptr(),
+                                       u_scales.data_ptr(), batch, M, F, K, ld, code,
+                                       _ELEM_DTYPES[dtype], _current_stream(_current_device()))
+    if rc < 0:
+        _check(rc)
     return out
