@@ -74,6 +74,8 @@ enum Src : int { kRows, kTrans, kPacked2, kPackedT2, kCodes, kCodes2 };
 enum Epi : int { kStore, kGated };
 
 constexpr uint32_t kXcds = 8;
+// M tiles in a band: an XCD works on 4 x 8 tiles at a time, whose 12 panels share
+// its L2. Gated 8192 x 4096 -> 8192: 4 746 us, 8 756, 16 763, 32 799.
 constexpr uint32_t kGroupM = 4;
 constexpr int kTileWaves = 4;
 constexpr int kBufferFlags = 0x00020000;           // raw, untyped buffer
@@ -118,7 +120,7 @@ struct TileAt {
 };
 
 // Linear workgroup id -> work index, each XCD taking a contiguous run. (All of
-// these fit 32 bits; 64-bit divisions took 1-2 us of every workgroup.)
+// these fit 32 bits; 64-bit divisions took about 1 us of every workgroup.)
 __device__ __forceinline__ uint32_t xcd_run(uint32_t w, uint32_t n) {
   const uint32_t q = n / kXcds, r = n % kXcds;
   const uint32_t xcd = w % kXcds, k = w / kXcds;
