@@ -34,13 +34,15 @@ constexpr int64_t kNoRow = int64_t(1) << 62;
 
 int64_t padded_width(int64_t F) { return (F + 31) / 32 * 32; }
 
-// Layout of the backward pass's workspace: [dG | dU], then the partial sums of
-// one product at a time. dX's rows are made in two launches where a first part
+// Layout of the backward pass's workspace: [dG | dU], the factor that undoes their
+// scaling and the peaks that it comes from (f16; kept for both types, so that a
+// workspace serves either), then from slopes_bytes on the partial sums of one product
+// at a time. dX's rows are made in two launches where a first part
 // fills the chip in whole rounds of large tiles and the few rows left would cost
 // another round: 32773 x 512, summed over 2048 values, 76 us against 90 (128 x 128
 // tiles) and 98 (256 x 256) in one.
 struct BackwardPlan {
-  int64_t slopes_bytes, need;
+  int64_t dgu_bytes, slopes_bytes, need;
   int64_t dx_rows;              // rows of the first launch
   bmm::TilePlan dx, dx_rest, dw;
 };
@@ -50,7 +52,9 @@ constexpr double kLaunchNs = 4000;
 BackwardPlan plan_backward(const bmm_gated_desc& d) {
   BackwardPlan p;
   const int64_t Fp2 = 2 * padded_width(d.F);
-  p.slopes_bytes = (d.batch * d.M * Fp2 * 2 + 255) / 256 * 256;
+  p.dgu_bytes = d.batch * d.M * Fp2 * 2;
+  const int64_t peaks = bmm::gated_peaks(d.batch * d.M, d.F);
+  p.slopes_bytes = (p.dgu_bytes + (peaks > 0 ? 4 * (1 + peaks) : 0) + 255) / 256 * 256;
   p.dx = p.dx_rest = bmm::plan_tiles(d.batch, d.M, d.K, Fp2 / 32, true);
   p.dx_rows = d.M;
   const int64_t across = (d.K + 255) / 256, down = across > 0 ? 256 / across : 0;
@@ -142,8 +146,14 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
     float* const part =
         reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.slopes_bytes);
     const int64_t Fp = padded_width(d.F);
+    float* rescale = nullptr;   // (no [dG | dU]: no factor either)
+    uint32_t* peaks = nullptr;
+    if (plan.dgu_bytes > 0) {
+      rescale = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.dgu_bytes);
+      peaks = reinterpret_cast<uint32_t*>(rescale + 1);
+    }
     int rc = hip_status(bmm::launch_gated_slopes(dgu, dH, G, U, d.batch * d.M, d.F, d.ld_h,
-                                                 d.dtype, d.act, s),
+                                                 d.dtype, d.act, peaks, rescale, s),
                         "gated_backward slopes launch");
     if (rc != BMM_OK) return rc;
     auto rows_of_dx = [&](int64_t row, int64_t rows, const bmm::TilePlan& tiles) {
@@ -164,6 +174,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.splits = tiles.splits;
       a.part = part;
       a.part_floats = d.batch * rows * d.K;
+      a.rescale = rescale;
       return hip_status(bmm::launch_gated_dx(a, d.dtype, s), "gated_backward dX launch");
     };
     if (dX && d.M > 0) {
@@ -190,6 +201,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.splits = plan.dw.splits;
       a.part = part;
       a.part_floats = d.batch * 2 * Fp * d.K;
+      a.rescale = rescale;
       rc = hip_status(bmm::launch_gated_dw(a, d.dtype, s), "gated_backward dW launch");
     }
     return rc;

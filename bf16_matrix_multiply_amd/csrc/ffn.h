@@ -48,15 +48,19 @@ struct TileArgs {
   int splits;
   float* part;
   int64_t part_floats;
+  const float* rescale;     // f16 store: the sums are multiplied by this power of two (null: 1)
 };
 
 // ---- launchers ----
 hipError_t launch_gated(const TileArgs& a, int dtype, hipStream_t s);
 // dG = dH U act'(G), dU = dH act(G), rounded to the operands' type, as (rows, 2 Fp) row-major
-// [dG | dU], Fp = F rounded up to 32 with zeros in between.
+// [dG | dU], Fp = F rounded up to 32 with zeros in between. f16: multiplied by a power of
+// two that suits its range; *rescale receives the one that undoes it, and peaks (so many
+// words, gated_peaks) is scratch memory.
+int64_t gated_peaks(int64_t rows, int64_t F);
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, hipStream_t s);
+                               int act, uint32_t* peaks, float* rescale, hipStream_t s);
 hipError_t launch_gated_dx(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t batch,

@@ -705,12 +705,18 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
       __builtin_amdgcn_raw_buffer_store_b128(v, SRCA == kTrans && i >= second ? to1 : to,
                                              at[j] + i * step, 0, decltype(nt)::value);
     };
+    float rescale = 1.f;
+    if constexpr (DT == kF16) rescale = p.rescale ? *p.rescale : 1.f;
+    auto result = [&](f32x4 acc) {
+      const f32x4 v = sum(acc);
+      return DT == kF16 ? v * rescale : v;
+    };
     auto store16 = [&](auto type) {
 #pragma unroll
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
-          store(i, j, join16<decltype(type)::value>(sum(acc[i][2 * j]), sum(acc[i][2 * j + 1])),
+          store(i, j, join16<decltype(type)::value>(result(acc[i][2 * j]), result(acc[i][2 * j + 1])),
                 std::integral_constant<int, kNonTemporal>{});
     };
     auto store32 = [&](auto nt) {

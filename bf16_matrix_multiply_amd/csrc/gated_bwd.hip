@@ -7,9 +7,14 @@
 // along its rows, the weight gradients along its columns. Rounding dG and dU
 // to the operands' type is what lets the matrix cores multiply them; the error
 // it adds to a gradient (a half step of each of many independent terms) is the
-// size of that gradient's own last rounding. No operand is transposed or
-// repacked in memory: the products read X, [dG | dU] and the packed weights
-// through the transposing LDS reads.
+// size of that gradient's own last rounding. For f16 that holds only inside its
+// range (2^-14 to 65504), which products of three f16 values leave on both
+// sides: a pass before finds the largest finite magnitude of dG and dU, both are
+// multiplied by the power of two that brings it to [2^14, 2^15), and the products
+// take that out of their float32 sums, which is exact. Values down to 2^-28 of the
+// largest then keep all their digits, and what vanishes is below 2^-39 of it. No
+// operand is transposed or repacked in memory: the products read X, [dG | dU]
+// and the packed weights through the transposing LDS reads.
 #include "ffn_tile.h"
 
 namespace bmm {
@@ -17,40 +22,108 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// dG and dU of 8 columns in one row, at element `at` of dH, G and U: fn(w, e, dG, dU)
+// for the values of each word.
+template <int DT, int ACT, class Fn>
+__device__ __forceinline__ void slopes_of_eight(const uint16_t* dh, const uint16_t* g,
+                                                const uint16_t* u, int64_t at, Fn fn) {
+  const u32x4 vh = *reinterpret_cast<const u32x4*>(dh + at);
+  const u32x4 vg = *reinterpret_cast<const u32x4*>(g + at);
+  const u32x4 vu = *reinterpret_cast<const u32x4*>(u + at);
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t sh = 16 * e;
+      const float h = half_bits_to_f32<DT>((vh[w] >> sh) & 0xffffu);
+      const float x = half_bits_to_f32<DT>((vg[w] >> sh) & 0xffffu);
+      const float y = half_bits_to_f32<DT>((vu[w] >> sh) & 0xffffu);
+      float a, slope;
+      act_and_slope<ACT>(x, a, slope);
+      fn(w, e, h * y * slope, h * a);
+    }
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The largest of the workgroup's values, in every thread.
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+  __shared__ uint32_t of_wave[kThreads / kWave];
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) x = umax(x, uint32_t(__shfl_xor(int(x), d, kWave)));
+  if (threadIdx.x % kWave == 0) of_wave[threadIdx.x / kWave] = x;
+  __syncthreads();
+  x = of_wave[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / kWave; ++w) x = umax(x, of_wave[w]);
+  return x;
+}
+
+// The largest finite magnitude of dG and dU that each workgroup meets, as float32
+// bits (which are ordered like the values). Bound by memory: 8192 x 8192 79 us = 5.1 TB/s;
+// of the whole backward pass 45 x 528 -> 1368 3 of 25 us, 32773 x 512 -> 1024 45 of 238.
+template <int DT, int ACT>
+__global__ __launch_bounds__(kThreads) void peaks_kernel(uint32_t* __restrict__ peaks,
+                                                         const uint16_t* __restrict__ dh,
+                                                         const uint16_t* __restrict__ g,
+                                                         const uint16_t* __restrict__ u, int64_t n,
+                                                         int64_t F, int64_t ld) {
+  const int64_t stride = int64_t(gridDim.x) * kThreads;
+  const int64_t per_row = F / 8;
+  uint32_t top = 0;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
+    const int64_t row = i / per_row, f = 8 * (i % per_row);
+    slopes_of_eight<DT, ACT>(dh, g, u, row * ld + f, [&](int, int, float dg, float du) {
+      const uint32_t a = __builtin_bit_cast(uint32_t, dg) & 0x7fffffffu;
+      const uint32_t b = __builtin_bit_cast(uint32_t, du) & 0x7fffffffu;
+      top = umax(top, umax(a < 0x7f800000u ? a : 0u, b < 0x7f800000u ? b : 0u));
+    });
+  }
+  top = block_max(top);
+  if (threadIdx.x == 0) peaks[blockIdx.x] = top;
+}
+
 // One thread: 8 columns of dG and of dU in one row. Read dH, G and U once, write
 // both halves: 10 bytes a column. Bound by memory: 8192 x 8192 113 us = 5.9 TB/s.
+// f16: the values are scaled as above by the largest of n_peaks peaks, and rescale
+// receives the factor that undoes it.
 template <int DT, int ACT>
 __global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__ dgu,
                                                           const uint16_t* __restrict__ dh,
                                                           const uint16_t* __restrict__ g,
                                                           const uint16_t* __restrict__ u,
                                                           int64_t n, int64_t F, int64_t Fp,
-                                                          int64_t ld) {
+                                                          int64_t ld,
+                                                          const uint32_t* __restrict__ peaks,
+                                                          int n_peaks,
+                                                          float* __restrict__ rescale) {
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t per_row = Fp / 8;
+  float scale = 1.f;
+  if constexpr (DT == kF16) {
+    uint32_t top = 0;
+    for (int i = threadIdx.x; i < n_peaks; i += kThreads) top = umax(top, peaks[i]);
+    top = block_max(top);
+    // 2^k with k = 14 - floor(log2 top); held at 2^126, so that 2^-k is a normal float
+    // (f16 operands give -18 at the least)
+    const int k = 14 + 127 - int(top >> 23), held = k < 126 ? k : 126;
+    scale = __builtin_bit_cast(float, uint32_t(127 + held) << 23);
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+      *rescale = __builtin_bit_cast(float, uint32_t(127 - held) << 23);
+  }
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
     const int64_t row = i / per_row, f = 8 * (i % per_row);
     u32x4 og = {0, 0, 0, 0}, ou = {0, 0, 0, 0};
     if (f < F) {
-      const u32x4 vh = *reinterpret_cast<const u32x4*>(dh + row * ld + f);
-      const u32x4 vg = *reinterpret_cast<const u32x4*>(g + row * ld + f);
-      const u32x4 vu = *reinterpret_cast<const u32x4*>(u + row * ld + f);
+      float dg[4][2], du[4][2];
+      slopes_of_eight<DT, ACT>(dh, g, u, row * ld + f, [&](int w, int e, float a, float b) {
+        dg[w][e] = DT == kF16 ? a * scale : a;
+        du[w][e] = DT == kF16 ? b * scale : b;
+      });
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        float dg[2], du[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t sh = 16 * e;
-          const float h = half_bits_to_f32<DT>((vh[w] >> sh) & 0xffffu);
-          const float x = half_bits_to_f32<DT>((vg[w] >> sh) & 0xffffu);
-          const float y = half_bits_to_f32<DT>((vu[w] >> sh) & 0xffffu);
-          float a, slope;
-          act_and_slope<ACT>(x, a, slope);
-          dg[e] = h * y * slope;
-          du[e] = h * a;
-        }
-        og[w] = pack2<DT>(dg[0], dg[1]);
-        ou[w] = pack2<DT>(du[0], du[1]);
+        og[w] = pack2<DT>(dg[w][0], dg[w][1]);
+        ou[w] = pack2<DT>(du[w][0], du[w][1]);
       }
     }
     uint16_t* out = dgu + row * 2 * Fp + f;
@@ -59,7 +132,8 @@ __global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__
   }
 }
 
-// The partial sums of a split product, added in order and rounded once. Rows
+// The partial sums of a split product, added in order and rounded once (f16: after
+// the factor at p.rescale). Rows
 // as in TileArgs: r < rows0 to d, row1 <= r < row1 + rows0 to d1.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void join_kernel(TileArgs p, int64_t n8) {
@@ -75,6 +149,11 @@ __global__ __launch_bounds__(kThreads) void join_kernel(TileArgs p, int64_t n8) 
       const float* at = p.part + s * p.part_floats + 8 * i;
       lo += load16f_nt(at);
       hi += load16f_nt(at + 4);
+    }
+    if constexpr (DT == kF16) {
+      const float z = p.rescale ? *p.rescale : 1.f;
+      lo *= z;
+      hi *= z;
     }
     const u32x4 o = {pack2<DT>(lo[0], lo[1]), pack2<DT>(lo[2], lo[3]), pack2<DT>(hi[0], hi[1]),
                      pack2<DT>(hi[2], hi[3])};
@@ -104,23 +183,36 @@ hipError_t product(const TileArgs& a, hipStream_t s) {
 
 }  // namespace
 
+int64_t gated_peaks(int64_t rows, int64_t F) {
+  const int64_t blocks = (rows * F / 8 + kThreads - 1) / kThreads;
+  return blocks < 1024 ? blocks : 1024;   // four workgroups a CU keep the memory busy
+}
+
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, hipStream_t s) {
+                               int act, uint32_t* peaks, float* rescale, hipStream_t s) {
   const int64_t Fp = (F + 31) / 32 * 32, n = rows * Fp / 8;
   if (n == 0) return hipSuccess;
-  auto pick = [&](auto dt) {
-    constexpr int DT = decltype(dt)::value;
+  auto by_act = [&](auto fn) {
     switch (act) {
-      case BMM_ACT_SILU: return slopes_kernel<DT, BMM_ACT_SILU>;
-      case BMM_ACT_GELU: return slopes_kernel<DT, BMM_ACT_GELU>;
-      case BMM_ACT_GELU_TANH: return slopes_kernel<DT, BMM_ACT_GELU_TANH>;
-      default: return slopes_kernel<DT, BMM_ACT_RELU>;
+      case BMM_ACT_SILU: return fn(std::integral_constant<int, BMM_ACT_SILU>{});
+      case BMM_ACT_GELU: return fn(std::integral_constant<int, BMM_ACT_GELU>{});
+      case BMM_ACT_GELU_TANH: return fn(std::integral_constant<int, BMM_ACT_GELU_TANH>{});
+      default: return fn(std::integral_constant<int, BMM_ACT_RELU>{});
     }
   };
-  auto kern = dtype == kBF16 ? pick(std::integral_constant<int, kBF16>{})
-                             : pick(std::integral_constant<int, kF16>{});
-  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld);
+  const int n_peaks = int(gated_peaks(rows, F));
+  if (dtype == kF16) {
+    hipLaunchKernelGGL(by_act([](auto a) { return peaks_kernel<kF16, decltype(a)::value>; }),
+                       dim3(unsigned(n_peaks)), dim3(kThreads), 0, s, peaks, dh, g, u, rows * F / 8,
+                       F, ld);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  auto kern = dtype == kBF16 ? by_act([](auto a) { return slopes_kernel<kBF16, decltype(a)::value>; })
+                             : by_act([](auto a) { return slopes_kernel<kF16, decltype(a)::value>; });
+  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld, peaks,
+                     n_peaks, rescale);
   return hipGetLastError();
 }
 

@@ -475,7 +475,12 @@ int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const ui
  * dH, G, U   (batch, M, ld_h); X (batch, M, ld_x); Wg, Wu as bmm_gated (may be
  *            NULL when dX is).
  * dG and dU are rounded to dtype before they are multiplied; sums are
- * float32, each gradient is rounded once. The result is the same on every run.
+ * float32, each gradient is rounded once. For f16, dG and dU are held times a
+ * power of two that brings the largest finite magnitude of the call to [2^14,
+ * 2^15), and the sums are divided by it: values down to 2^-28 of the largest
+ * keep f16's 11 digits, those below 2^-39 of it count as zero, and no finite
+ * value overflows before a gradient's own rounding does. The result is the
+ * same on every run.
  * workspace  device memory of at least bmm_gated_backward_workspace_bytes(desc)
  *            bytes, 16-byte aligned, overlapping nothing else; owned by the
  *            caller, clobbered.
