@@ -1,10 +1,10 @@
 """Python binding of libbmm.so: the tiled f16/bf16 multiply-accumulate
 D = A * B^T + C on MI355X (gfx950).
 
-Argument marshalling only. Each function takes torch tensors on the GPU, reads
-their pointers, extents and the current torch stream, and calls the C ABI of
-``include/bmm.h`` with the same name; every step of the computation runs in
-the library's HIP kernels. If the library is not built, every call raises;
+Argument marshalling only. Each function takes torch tensors on one GPU, reads
+their pointers, extents and that GPU's current torch stream, and calls the C
+ABI of ``include/bmm.h`` with the same name; every step of the computation runs
+in the library's HIP kernels. If the library is not built, every call raises;
 there is no other code path.
 
 Layouts (mma.sync page of the TVM tirx tile-op documentation, "Operand
@@ -19,6 +19,7 @@ containers).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import typing
 
@@ -189,11 +190,42 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _require_cuda(*ts):
+    """Every given tensor is on a GPU, and all on the same one."""
+    device = None
     for t in ts:
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("bmm operates on GPU tensors only")
+        if device is not None and t.device != device:
+            raise ValueError(f"bmm operates on tensors of one GPU, got {device} and {t.device}")
+        device = t.device
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on_gpu(device, fn, *args):
+    """fn with that GPU as the current one: what it enqueues goes to its current
+    stream."""
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _on_its_gpu(fn):
+    """fn, run on the GPU of its first tensor."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        t = args[0] if args else next((v for v in kw.values() if isinstance(v, torch.Tensor)), None)
+        device = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if device < 0 or device == _current_device():   # (the CPU: fn refuses it)
+            return fn(*args, **kw)
+        return _on_gpu(device, functools.partial(fn, **kw), *args)
+    return call
+
+
+@_on_its_gpu
 def pack_operand(x: torch.Tensor, atom_rows: int, K: int | None = None,
                  out: torch.Tensor | None = None, atom_k: int = 16) -> torch.Tensor:
     """Row-major (batch, rows, ld) or (rows, ld) 16-bit tensor -> packed words
@@ -204,7 +236,7 @@ def pack_operand(x: torch.Tensor, atom_rows: int, K: int | None = None,
     with batches ``rows * ld`` apart; K (default ld) may be smaller than ld."""
     if atom_k not in (16, 8):
         raise ValueError("pack_operand: atom_k must be 16 or 8")
-    _require_cuda(x)
+    _require_cuda(x, out)
     if x.element_size() != 2:
         raise ValueError("pack_operand takes 16-bit (f16/bf16 bit) tensors")
     if x.dim() == 2:
@@ -225,6 +257,7 @@ def pack_operand(x: torch.Tensor, atom_rows: int, K: int | None = None,
     return out
 
 
+@_on_its_gpu
 def pack_operand_kmajor(xt: torch.Tensor, atom_rows: int, rows: int | None = None,
                         out: torch.Tensor | None = None, atom_k: int = 16) -> torch.Tensor:
     """K-major (batch, K, ld) or (K, ld) 16-bit tensor holding element (row, k)
@@ -233,7 +266,7 @@ def pack_operand_kmajor(xt: torch.Tensor, atom_rows: int, rows: int | None = Non
     for bmm_pack_operand_kmajor_k8). rows defaults to ld."""
     if atom_k not in (16, 8):
         raise ValueError("pack_operand_kmajor: atom_k must be 16 or 8")
-    _require_cuda(xt)
+    _require_cuda(xt, out)
     if xt.element_size() != 2:
         raise ValueError("pack_operand_kmajor takes 16-bit (f16/bf16 bit) tensors")
     if xt.dim() == 2:
@@ -253,6 +286,7 @@ def pack_operand_kmajor(xt: torch.Tensor, atom_rows: int, rows: int | None = Non
     return out
 
 
+@_on_its_gpu
 def box_copy(src: torch.Tensor, box, coords, n_repeat: int = 1, coord_step=None,
              swizzle: int = 0, dims=None, strides=None, oob_fill: int = 0,
              out: torch.Tensor | None = None):
@@ -260,7 +294,7 @@ def box_copy(src: torch.Tensor, box, coords, n_repeat: int = 1, coord_step=None,
 
     dims/strides default to ``src``'s own extents and byte strides (outer to
     inner); strides are in bytes."""
-    _require_cuda(src)
+    _require_cuda(src, out)
     d = _box_desc(src, box, coords, n_repeat, coord_step, swizzle, dims, strides, oob_fill)
     shape = (n_repeat, *box)
     if out is None:
@@ -289,6 +323,7 @@ def _box_desc(t: torch.Tensor, box, coords, n_repeat, coord_step, swizzle, dims,
     return d
 
 
+@_on_its_gpu
 def box_store(dst: torch.Tensor, image: torch.Tensor, box, coords, n_repeat: int = 1,
               coord_step=None, swizzle: int = 0, dims=None, strides=None) -> int:
     """Write the compact (n_repeat, *box) ``image`` into ``dst``'s boxes (in place;
@@ -303,6 +338,7 @@ def box_store(dst: torch.Tensor, image: torch.Tensor, box, coords, n_repeat: int
     return nbytes.value
 
 
+@_on_its_gpu
 def box_reduce_add(dst: torch.Tensor, image: torch.Tensor, box, coords, elem_type: str,
                    n_repeat: int = 1, coord_step=None, swizzle: int = 0, dims=None,
                    strides=None) -> int:
@@ -333,6 +369,7 @@ def splitk_suggested(batch, M_rep, N_rep, K_rep, atom_k=16) -> int:
     return _check(lib().bmm_splitk_suggested(batch, M_rep, N_rep, K_rep, atom_k))
 
 
+@_on_its_gpu
 def mma_tile_splitk(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None,
                     c: float = 0.0, dtype=None, splits: int | None = None,
                     out: torch.Tensor | None = None,
@@ -378,6 +415,7 @@ def mma_tile_splitk(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = N
     return out
 
 
+@_on_its_gpu
 def mma_tile_splitk_noalloc(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None,
                             c: float = 0.0, dtype=None, splits: int | None = None,
                             out: torch.Tensor | None = None) -> torch.Tensor:
@@ -415,6 +453,7 @@ def mma_tile_splitk_noalloc(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | 
     return out
 
 
+@_on_its_gpu
 def mma_tile(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None,
              c: float = 0.0, dtype=None, out: torch.Tensor | None = None,
              kernel: str = "auto", alpha: float | None = None,
@@ -486,15 +525,6 @@ def _act_code(act: str, fn: str) -> int:
 # the common case of each check below comes first and costs a few attribute
 # reads; the slow path names the fault.
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _raw_stream() -> int:
-    """The current device's current torch stream, as the C ABI takes it."""
-    return _current_stream(_current_device())
-
-
 def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
@@ -564,7 +594,10 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
     the same type. Returns H (..., M, F) in X's type, and with ``save`` (H, G,
     U), the projections that gated_backward takes. ``act`` is one of ACTS."""
     code = _act_code(act, "gated")
-    if not (X.is_cuda and Wg.is_cuda and Wu.is_cuda and out is None):
+    device = X.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, gated, X, Wg, Wu, act, save, out)
+    if not (out is None and 0 <= device == Wg.get_device() == Wu.get_device()):
         _require_cuda(X, Wg, Wu, out)
     dt = _half_matrix(X, "X", "gated")
     ld_x = _rows_ld(X, "X", "gated")
@@ -580,7 +613,7 @@ def gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu"
     d = GatedDesc(batch, M, F, K, ld_x, ld_h, dt, code)
     rc = (_lib or lib()).bmm_gated(H.data_ptr(), _addr(G), _addr(U), X.data_ptr(), Wg.data_ptr(),
                                    Wu.data_ptr(), ctypes.byref(d),
-                                   _current_stream(_current_device()))
+                                   _current_stream(device))
     if rc < 0:
         _check(rc)
     return (H, G, U) if save else H
@@ -592,6 +625,7 @@ def gated_backward_workspace_bytes(batch: int, M: int, F: int, K: int) -> int:
     return _check(lib().bmm_gated_backward_workspace_bytes(ctypes.byref(d)))
 
 
+@_on_its_gpu
 def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.Tensor,
                    Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", need_dx: bool = True,
                    need_dw: bool = True, workspace: torch.Tensor | None = None):
@@ -633,7 +667,8 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.
         dWu = X.new_empty((*lead, F, K))
     _check(lib().bmm_gated_backward(_addr(dX), _addr(dWg), _addr(dWu), _addr(dH), _addr(G), _addr(U),
                                     _addr(X), _addr(Wg), _addr(Wu), ctypes.byref(d), _addr(workspace),
-                                    workspace.numel() * workspace.element_size(), _raw_stream()))
+                                    workspace.numel() * workspace.element_size(),
+                                    _current_stream(_current_device())))
     return dX, dWg, dWu
 
 
@@ -665,7 +700,7 @@ def _mx4_check(op: Mx4Operand, name, fn) -> int:
     want = _mx4_shapes(batch, rows, K)
     if codes.shape == want[0] and scales.shape == want[1] and codes.dtype == scales.dtype == \
             torch.uint8 and codes.is_contiguous() and scales.is_contiguous() and \
-            codes.is_cuda and scales.is_cuda and (batched or batch == 1):
+            0 <= codes.get_device() == scales.get_device() and (batched or batch == 1):
         return batch
     for t, shape, part in ((codes, want[0], "codes"), (scales, want[1], "scales")):
         if t.shape != shape or t.dtype != torch.uint8 or not t.is_contiguous():
@@ -680,6 +715,9 @@ def mx4_quantize(X: torch.Tensor) -> Mx4Operand:
     operand (bmm_mx4_quantize): blocks of 32 along K, one power-of-two scale
     each. K is a multiple of 32; rows may be any multiple of 8 elements apart."""
     fn = "mx4_quantize"
+    device = X.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, mx4_quantize, X)
     if not X.is_cuda:
         _require_cuda(X)
     elem = _ELEM_DTYPES.get(X.dtype)
@@ -692,7 +730,7 @@ def mx4_quantize(X: torch.Tensor) -> Mx4Operand:
     codes = X.new_empty(cs, dtype=torch.uint8)
     scales = codes.new_empty(ss)
     rc = (_lib or lib()).bmm_mx4_quantize(codes.data_ptr(), scales.data_ptr(), X.data_ptr(), batch,
-                                          rows, K, ld, elem, _current_stream(_current_device()))
+                                          rows, K, ld, elem, _current_stream(device))
     if rc < 0:
         _check(rc)
     return Mx4Operand(codes, scales, rows, K, bool(lead))
@@ -704,8 +742,11 @@ def mx4_dequantize(A: Mx4Operand, dtype: torch.dtype = torch.float32,
     (bmm_mx4_dequantize)."""
     fn = "mx4_dequantize"
     batch = _mx4_check(A, "A", fn)
+    device = A.codes.get_device()
+    if device != _current_device():
+        return _on_gpu(device, mx4_dequantize, A, dtype, out)
     if out is not None:
-        _require_cuda(out)
+        _require_cuda(A.codes, out)
     elem = _ELEM_DTYPES.get(dtype)
     if elem is None:
         raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
@@ -713,7 +754,7 @@ def mx4_dequantize(A: Mx4Operand, dtype: torch.dtype = torch.float32,
     out, ld = _out(out, (batch, rows, K) if batched else (rows, K), dtype, codes, fn)
     rc = (_lib or lib()).bmm_mx4_dequantize(out.data_ptr(), codes.data_ptr(), scales.data_ptr(),
                                             batch, rows, K, ld, elem,
-                                            _current_stream(_current_device()))
+                                            _current_stream(device))
     if rc < 0:
         _check(rc)
     return out
@@ -727,8 +768,11 @@ def mx4_mma(A: Mx4Operand, B: Mx4Operand, dtype: torch.dtype = torch.float32,
     fn = "mx4_mma"
     batch = _mx4_check(A, "A", fn)
     batch_b = _mx4_check(B, "B", fn)
-    if out is not None:
-        _require_cuda(out)
+    device = A.codes.get_device()
+    if device != _current_device():
+        return _on_gpu(device, mx4_mma, A, B, dtype, out)
+    if out is not None or B.codes.get_device() != device:
+        _require_cuda(A.codes, B.codes, out)
     elem = _ELEM_DTYPES.get(dtype)
     if elem is None:
         raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
@@ -739,7 +783,7 @@ def mx4_mma(A: Mx4Operand, B: Mx4Operand, dtype: torch.dtype = torch.float32,
     out, ld = _out(out, (batch, M, N) if batched else (M, N), dtype, a, fn)
     rc = (_lib or lib()).bmm_mx4_mma(out.data_ptr(), a.data_ptr(), a_scales.data_ptr(), b.data_ptr(),
                                      b_scales.data_ptr(), batch, M, N, K, ld, elem,
-                                     _current_stream(_current_device()))
+                                     _current_stream(device))
     if rc < 0:
         _check(rc)
     return out
@@ -755,8 +799,11 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     code = _act_code(act, fn)
     batch = _mx4_check(X, "X", fn)
     batch_g, batch_u = _mx4_check(Wg, "Wg", fn), _mx4_check(Wu, "Wu", fn)
-    if out is not None:
-        _require_cuda(out)
+    device = X.codes.get_device()
+    if device != _current_device():
+        return _on_gpu(device, mx4_gated, X, Wg, Wu, act, dtype, out)
+    if not (out is None and device == Wg.codes.get_device() == Wu.codes.get_device()):
+        _require_cuda(X.codes, Wg.codes, Wu.codes, out)
     if dtype not in _HALF_DTYPES:
         raise ValueError(f"{fn}: dtype must be float16 or bfloat16, got {dtype}")
     x, x_scales, M, K, batched = X
@@ -770,7 +817,7 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     rc = (_lib or lib()).bmm_mx4_gated(out.data_ptr(), x.data_ptr(), x_scales.data_ptr(),
                                        g.data_ptr(), g_scales.data_ptr(), u.data_ptr(),
                                        u_scales.data_ptr(), batch, M, F, K, ld, code,
-                                       _ELEM_DTYPES[dtype], _current_stream(_current_device()))
+                                       _ELEM_DTYPES[dtype], _current_stream(device))
     if rc < 0:
         _check(rc)
     return out
