@@ -69,8 +69,9 @@ Status all_given(const char* what, std::initializer_list<Rows> ps) {
   return Status{};
 }
 
-constexpr int64_t kMaxK = int64_t(1) << 22;    // below it
-constexpr int64_t kMaxLd = int64_t(1) << 21;   // 32-bit offsets inside a tile's rows
+constexpr int64_t kMaxK = int64_t(1) << 22;    // below it (4-bit operands)
+constexpr int64_t kMaxLd = int64_t(1) << 21;   // 32-bit offsets inside a tile's rows; the gated
+                                               // block's K is such a distance too (dX, dWg, dWu)
 constexpr int64_t kMaxF = int64_t(1) << 20;
 
 int elem_size(int32_t t) {
@@ -87,8 +88,8 @@ Status check_gated_desc(const bmm_gated_desc* d, const char* what) {
     return failw(what, BMM_EINVAL, "act %lld is not a bmm_act", d->act);
   if (d->batch < 0 || d->M < 0 || d->F < 0 || d->K < 0)
     return failw(what, BMM_EINVAL, "negative extent");
-  if (d->batch > kMaxExtent || d->M > kMaxExtent || d->F > kMaxF || d->K >= kMaxK)
-    return failw(what, BMM_EINVAL, "extent too large (F <= 2^20, K < 2^22)");
+  if (d->batch > kMaxExtent || d->M > kMaxExtent || d->F > kMaxF || d->K > kMaxLd)
+    return failw(what, BMM_EINVAL, "extent too large (F <= 2^20, K <= 2^21)");
   if (d->F % 8) return failw(what, BMM_EINVAL, "F (%lld) is not a multiple of 8", d->F);
   if (d->K % 16) return failw(what, BMM_EINVAL, "K (%lld) is not a multiple of 16", d->K);
   if (d->ld_x < d->K) return failw(what, BMM_EINVAL, "ld_x (%lld) < K (%lld)", d->ld_x, d->K);

@@ -428,7 +428,7 @@ typedef enum {
  *   batch  independent blocks (each with its own weights)
  *   M      rows of X (tokens); any
  *   F      width of the block, a multiple of 8, at most 2^20
- *   K      width of X, a multiple of 16, below 2^22
+ *   K      width of X, a multiple of 16, at most 2^21
  *   ld_x   elements between rows of X: >= K, a multiple of 8, at most 2^21
  *   ld_h   elements between rows of H, G, U and dH: >= F, a multiple of 8, at
  *          most 2^21
