@@ -100,8 +100,9 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
     const auto ra = buffer(base_a + q * (kSteps * kBytesA));
     const int64_t left64 = p.K - q * (kSteps * kValues);
     const int left = int(left64 < kSteps * kValues ? left64 : kSteps * kValues);
-    // (the last round may be short: a lane past the end, by its first value, reads zeros)
-    const int first = k4 ? 0 : 8 * g;
+    // (the last round may be short: a lane past the end, by its first value, reads zeros,
+    // and so not the codes that pad K to whole steps)
+    const int first = (k4 ? 32 : 8) * g;
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
       const bool ok = u * kValues + first < left;
