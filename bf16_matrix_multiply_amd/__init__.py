@@ -30,7 +30,8 @@ __all__ = ["BmmError", "pack_operand", "pack_operand_kmajor", "box_copy", "box_s
            "splitk_default", "splitk_suggested", "NOALLOC_SCRATCH_BYTES",
            "splitk_workspace_bytes", "select_kernel", "library_path", "KERNELS", "MmaOpts",
            "ELEM_TYPES", "ACTS", "gated", "gated_backward", "gated_backward_workspace_bytes",
-           "Mx4Operand", "mx4_quantize", "mx4_dequantize", "mx4_mma", "mx4_gated"]
+           "ffn_plan", "FFN_PRODUCTS", "FFN_TILES", "Mx4Operand", "mx4_quantize", "mx4_dequantize",
+           "mx4_mma", "mx4_gated"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbmm.so")
@@ -42,9 +43,13 @@ KERNELS = {"auto": 0, "direct": 1, "tiled": 2, "skinny": 3, "tiled128": 4, "tile
 NOALLOC_SCRATCH_BYTES = 64 << 20   # BMM_NOALLOC_SCRATCH_BYTES
 ELEM_TYPES = {"f32": 1, "f16": 2, "bf16": 3, "i32": 4, "i64": 5}
 ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+FFN_PRODUCTS = {"gated": 0, "gated_dx": 1, "gated_dx_rest": 2, "gated_dw": 3, "mx4_mma": 4,
+                "mx4_gated": 5}
+FFN_TILES = {"128x128": 0, "256x128": 1, "256x192": 2, "256x256": 3, "few_rows": 4, "none": 5}
 _HALF_DTYPES = {torch.float16: BMM_F16, torch.bfloat16: BMM_BF16}
 _ELEM_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
+FFN_TILE_NAMES = {v: k for k, v in FFN_TILES.items()}
 
 
 class BmmError(RuntimeError):
@@ -154,8 +159,9 @@ def lib():
         L.bmm_mx4_dequantize.argtypes = [p, p, p, i64, i64, i64, i64, i32, p]
         L.bmm_mx4_mma.argtypes = [p] * 5 + [i64] * 5 + [i32, p]
         L.bmm_mx4_gated.argtypes = [p] * 7 + [i64] * 5 + [i32, i32, p]
-        for f in (L.bmm_gated, L.bmm_gated_backward, L.bmm_mx4_quantize, L.bmm_mx4_dequantize,
-                  L.bmm_mx4_mma, L.bmm_mx4_gated):
+        L.bmm_ffn_plan.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(i32)]
+        for f in (L.bmm_ffn_plan, L.bmm_gated, L.bmm_gated_backward, L.bmm_mx4_quantize,
+                  L.bmm_mx4_dequantize, L.bmm_mx4_mma, L.bmm_mx4_gated):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -670,6 +676,15 @@ def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.
                                     workspace.numel() * workspace.element_size(),
                                     _current_stream(_current_device())))
     return dX, dWg, dWu
+
+
+def ffn_plan(product: str, batch: int, M: int, F: int, K: int) -> tuple[str, int]:
+    """How a feed-forward product of these extents is made (bmm_ffn_plan): its tile, one
+    of FFN_TILES, and the number of parts that its sum is cut into. ``product`` is one
+    of FFN_PRODUCTS; F is N for "mx4_mma"."""
+    splits = ctypes.c_int32()
+    tile = _check(lib().bmm_ffn_plan(FFN_PRODUCTS[product], batch, M, F, K, ctypes.byref(splits)))
+    return FFN_TILE_NAMES[tile], splits.value
 
 
 class Mx4Operand(typing.NamedTuple):

@@ -80,6 +80,15 @@ BackwardPlan plan_backward(const bmm_gated_desc& d) {
   return p;
 }
 
+// The tile of a forward product: 16-bit gated, and the 4-bit product of N columns
+// (gated: of both weights together).
+int gated_tile(const bmm_gated_desc& d) {
+  return bmm::plan_forward(d.batch, d.M, 2 * d.F, d.K / 32);
+}
+int mx4_tile(int64_t batch, int64_t M, int64_t N, int64_t K) {
+  return bmm::plan_forward(batch, M, N, K / 128);
+}
+
 bmm::TileArgs gated_args(const bmm_gated_desc& d) {
   bmm::TileArgs a{};
   a.batch = d.batch;
@@ -114,7 +123,7 @@ int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const ui
     a.ldd = d.ld_h;
     a.a_bs = d.M * d.ld_x;
     a.b_bs = d.F * d.K;
-    a.tile = bmm::plan_forward(d.batch, d.M, 2 * d.F, d.K / 32);
+    a.tile = gated_tile(d);
     return hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
                       "gated launch");
   });
@@ -208,6 +217,34 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
   });
 }
 
+int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K,
+                 int32_t* splits) {
+  return guarded([&] {
+    const bool four = product == BMM_FFN_MX4_MMA || product == BMM_FFN_MX4_GATED;
+    const bmm_gated_desc d{batch, M, F, K, K, F, BMM_BF16, BMM_ACT_SILU};
+    const bmm::Status st = bmm::check_ffn_plan(product, d);
+    if (!st.ok()) return report(st);
+    bmm::TilePlan plan{BMM_TILE_NONE, 1, 0};
+    // (the backward pass writes the zeros of an empty sum: dX for F = 0, dWg and dWu for M = 0)
+    const bool forward = four || product == BMM_FFN_GATED, dw = product == BMM_FFN_GATED_DW;
+    if (batch == 0 || (forward ? M == 0 || F == 0 : K == 0 || (dw ? F : M) == 0))
+      ;   // nothing to make
+    else if (product == BMM_FFN_GATED)
+      plan.tile = gated_tile(d);
+    else if (four)
+      plan.tile = mx4_tile(batch, M, product == BMM_FFN_MX4_GATED ? 2 * F : F, K);
+    else {
+      const BackwardPlan b = plan_backward(d);
+      if (product == BMM_FFN_GATED_DX) plan = b.dx;
+      else if (dw) plan = b.dw;
+      else if (b.dx_rows < M) plan = b.dx_rest;
+    }
+    if (splits) *splits = plan.splits;
+    report(st);
+    return plan.tile;
+  });
+}
+
 int64_t bmm_mx4_codes_bytes(int64_t batch, int64_t rows, int64_t K) {
   const int64_t n = bmm::mx4_codes_bytes(batch, rows, K);
   return n < 0 ? BMM_EINVAL : n;
@@ -271,7 +308,7 @@ int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const 
     a.bs_bs = bmm::mx4_scales_bytes(1, N, K);
     a.out_type = elem_type;
     a.splits = 1;
-    a.tile = bmm::plan_forward(batch, M, N, K / 128);
+    a.tile = mx4_tile(batch, M, N, K);
     return hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
   });
 }
@@ -306,7 +343,7 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
     a.act = act;
     a.out_type = elem_type;
     a.splits = 1;
-    a.tile = bmm::plan_forward(batch, M, 2 * F, K / 128);
+    a.tile = mx4_tile(batch, M, 2 * F, K);
     return hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
                       "mx4_gated launch");
   });

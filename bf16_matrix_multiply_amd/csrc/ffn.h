@@ -17,7 +17,13 @@ enum : int { kMX4 = 2 };
 
 // How a product is made: by tiles of so many rows x columns (gated: columns of
 // both weights), or by the kernel for few rows (ffn_skinny.h).
-enum TileSize : int { kTile128, kTile256x128, kTile256x192, kTile256, kSkinny };
+enum TileSize : int {
+  kTile128 = BMM_TILE_128X128,
+  kTile256x128 = BMM_TILE_256X128,
+  kTile256x192 = BMM_TILE_256X192,
+  kTile256 = BMM_TILE_256X256,
+  kSkinny = BMM_TILE_FEW_ROWS
+};
 
 // One product D = A * B^T on MFMA tiles. Which fields count depends on how
 // the operands lie in memory and on the epilogue (ffn_tile.h).

@@ -58,6 +58,8 @@ Status check_gated_backward(const uint16_t* dX, const uint16_t* dWg, const uint1
 // Bytes of a 4-bit operand's codes and scales, or -1 for invalid extents.
 int64_t mx4_codes_bytes(int64_t batch, int64_t rows, int64_t K);
 int64_t mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K);
+// A product of bmm_ffn_plan (4 bits: F columns).
+Status check_ffn_plan(int32_t product, const bmm_gated_desc& d);
 // Quantise (`mat` is read) or dequantise (`mat` is written).
 Status check_mx4_convert(const void* mat, const uint8_t* codes, const uint8_t* scales,
                          int64_t batch, int64_t rows, int64_t K, int64_t ld, int32_t elem_type,

@@ -162,6 +162,19 @@ int64_t mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K) {
   return mul_capped({batch, (rows + 15) / 16, (K + 511) / 512, 256});
 }
 
+Status check_ffn_plan(int32_t product, const bmm_gated_desc& d) {
+  const char* what = "ffn_plan";
+  if (product < BMM_FFN_GATED || product > BMM_FFN_MX4_GATED)
+    return failw(what, BMM_EINVAL, "product %lld is not a bmm_ffn_product", product);
+  if (product != BMM_FFN_MX4_MMA && product != BMM_FFN_MX4_GATED) return check_gated_desc(&d, what);
+  if (d.F % 8) return failw(what, BMM_EINVAL, "%lld columns are not a multiple of 8", d.F);
+  if (d.K % 32) return failw(what, BMM_EINVAL, "K (%lld) is not a multiple of 32", d.K);
+  if (d.F > kMaxLd || mx4_codes_bytes(d.batch, d.M, d.K) < 0 ||
+      mx4_codes_bytes(d.batch, d.F, d.K) < 0)
+    return failw(what, BMM_EINVAL, "negative or too large (columns <= 2^21, K < 2^22)");
+  return Status{};
+}
+
 Status check_mx4_convert(const void* mat, const uint8_t* codes, const uint8_t* scales,
                          int64_t batch, int64_t rows, int64_t K, int64_t ld, int32_t elem_type,
                          const char* what) {

@@ -564,6 +564,35 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
                   const uint8_t* Wu_scales, int64_t batch, int64_t M, int64_t F, int64_t K,
                   int64_t ld_h, int32_t act, int32_t elem_type, void* stream);
 
+/*
+ * bmm_ffn_plan — how the product of these extents is made (diagnostics and
+ * tests): a bmm_ffn_tile, or < 0. *splits (may be NULL) receives the number of
+ * parts that its sum is cut into. F is the columns of D for BMM_FFN_MX4_MMA.
+ * The rows of dX may be made in two launches; BMM_FFN_GATED_DX is the first.
+ * BMM_TILE_NONE: there is nothing to make, or no second launch.
+ */
+typedef enum {
+  BMM_FFN_GATED = 0,
+  BMM_FFN_GATED_DX = 1,
+  BMM_FFN_GATED_DX_REST = 2,
+  BMM_FFN_GATED_DW = 3,
+  BMM_FFN_MX4_MMA = 4,
+  BMM_FFN_MX4_GATED = 5
+} bmm_ffn_product;
+
+/* Rows x columns of a tile (gated: columns of both weights together). */
+typedef enum {
+  BMM_TILE_128X128 = 0,
+  BMM_TILE_256X128 = 1,
+  BMM_TILE_256X192 = 2,
+  BMM_TILE_256X256 = 3,
+  BMM_TILE_FEW_ROWS = 4, /* up to 64 rows: the weights are read once */
+  BMM_TILE_NONE = 5
+} bmm_ffn_tile;
+
+int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K,
+                 int32_t* splits);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char* bmm_last_error(void);
 
