@@ -38,11 +38,25 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
   constexpr int kBytesB = k4 ? 1024 : 512;            // of a lane's row, from step to step
   constexpr int kBytesA = k4 ? 1024 : 64;
   // Whether the waves take the rounds in turns, so that together they read on in
-  // each row, or each a range of its own. Measured, in turns against ranges: 16-bit
-  // weights 22.4 / 23.8 us (one token, 4096 -> 8192), 21.4 / 31.6 (8192 -> 4096);
-  // 4-bit product 24.0 / 29.4 (16384 x 16384), but for 32 rows 22.1 / 17.6 (4096 x
-  // 16384) and 30.1 / 32.4 (16384 x 16384); 4-bit gated 27.2 / 25.0 (8192 -> 16384).
-  constexpr bool kTurns = !k4 || (EPI == kStore && MR == 1);
+  // each row, or each a range of its own. Measured, in turns / ranges (us, launches
+  // from a graph, weights cold):
+  //   rows                              1          16         32         64
+  //   16 bits, 4096 -> 8192             24.1/24.8  23.8/25.4  34.2/34.0  47.0/47.4
+  //   16 bits, 8192 -> 4096             26.3/27.9  27.2/28.2  38.6/38.0  47.4/48.1
+  //   16 bits, 2048 -> 5464             11.2/12.3  12.4/13.5  16.4/16.7  24.0/24.7
+  //   16 bits, 8192 -> 1024             14.6/14.2  17.5/17.4  31.8/31.2  41.8/41.5
+  //   4-bit product, 16384 -> 16384     24.8/27.5  24.7/28.6  29.1/33.2  32.4/34.4
+  //   4-bit product, 4096 -> 16384      8.5/8.5    8.6/8.6    10.5/10.3  12.5/12.5
+  //   4-bit product, 8192 -> 1024       5.6/5.6    6.3/6.3    10.6/10.6  13.7/13.8
+  //   4-bit gated, 8192 -> 16384        24.9/24.8  25.5/25.5  28.5/27.4  31.7/30.9
+  //   4-bit gated, 4096 -> 8192         8.6/8.7    8.6/8.7    10.8/10.8  12.4/12.4
+  //   4-bit gated, 2048 -> 5464         5.2/5.4    5.5/5.7    6.5/6.6    8.5/9.1
+  constexpr bool kTurns = !k4 || EPI == kStore;
+  // Whether the compiler is kept from moving products between a round's loads. 4-bit
+  // product, kept / not: one row 16384 -> 16384 24.8/27.0 us, 8192 -> 1024 5.6/7.6;
+  // 64 rows 32.4/36.6, 13.7/15.5. Gated: one row 8192 -> 16384 24.8/26.2, 8192 -> 1024
+  // 6.6/7.4, but 64 rows 35.0/30.9 (registers: two waves a SIMD instead of four).
+  constexpr bool kTogether = k4 && (EPI == kStore || MR == 1);
   __shared__ __attribute__((aligned(16))) f32x4 red[W / 2][MR][NB][kWave];
 
   const int lane = threadIdx.x & (kWave - 1);
@@ -100,19 +114,19 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
     const auto ra = buffer(base_a + q * (kSteps * kBytesA));
     const int64_t left64 = p.K - q * (kSteps * kValues);
     const int left = int(left64 < kSteps * kValues ? left64 : kSteps * kValues);
-    // (the last round may be short: a lane past the end, by its first value, reads zeros,
-    // and so not the codes that pad K to whole steps)
-    const int first = (k4 ? 32 : 8) * g;
+    // The last round may be short: a lane past the end, by its first value, reads zeros.
+    // (4 bits: so for X; the codes that pad the weights' K meet those zeros)
+    const int first = k4 ? 0 : 8 * g, first_a = (k4 ? 32 : 8) * g;
 #pragma unroll
     for (int u = 0; u < kSteps; ++u) {
-      const bool ok = u * kValues + first < left;
+      const bool ok = u * kValues + first < left, ok_a = u * kValues + first_a < left;
 #pragma unroll
       for (int j = 0; j < NB; ++j)
         fb[u][j] = load_at(EPI == kGated && (j & 1) ? rb1 : rb0,
                            ok ? ob[j] + u * kBytesB : kOutOfRange, 1);
 #pragma unroll
       for (int i = 0; i < MR; ++i)
-        fa[u][i] = load_at(ra, ok ? oa[i] + u * kBytesA : kOutOfRange, 0);
+        fa[u][i] = load_at(ra, ok_a ? oa[i] + u * kBytesA : kOutOfRange, 0);
     }
     if constexpr (k4) {
 #pragma unroll
@@ -121,6 +135,7 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
       for (int j = 0; j < NB; ++j)
         xb[j] = EPI == kGated ? cb[j & 1].word(j >> 1, q, lane) : cb[0].word(j, q, lane);
     }
+    if constexpr (kTogether) __builtin_amdgcn_sched_barrier(0);
     static_for<0, kSteps>([&](auto step) {
       constexpr int u = decltype(step)::value;
 #pragma unroll
