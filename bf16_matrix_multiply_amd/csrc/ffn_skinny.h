@@ -11,7 +11,7 @@
 // same result on every run.
 //
 // Measured on MI355X, weights cold: one token through 2 x 8192 x 4096 bf16 22.4 us =
-// 6.0 TB/s, through 16384 x 16384 4-bit weights 24 us = 5.8 TB/s; a long read
+// 6.0 TB/s, through 16384 x 16384 4-bit weights 23.7 us = 6.0 TB/s; a long read
 // reaches 6.5. Eight steps at a time, 16 waves, a second set of registers for the
 // next round, or loads that stay in the caches changed it by -1 to +4 us.
 //
@@ -218,11 +218,22 @@ hipError_t launch_skinny_of(const TileArgs& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Blocks a workgroup: two (512 workgroups for 8192 gated columns). For 4 bits and
-// more than 16 rows four, so that fewer workgroups read X: 24 x 16384 -> 16384
-// 32.3 against 34.5 us, gated 48 x 16384 -> 8192 29.3 against 41.7; 16-bit weights
-// have the better of two (gated 24 x 4096 -> 8192 29.9 against 34.9 us, 48 x 8192
-// -> 1024 38.2 against 59.4) but for 64 rows of the wide block (46.3 against 42.8).
+// Blocks a workgroup: two (512 workgroups for 8192 gated columns); for 4 bits and more
+// than 16 rows four, so that fewer workgroups read X. Two / four, us, launches from a
+// graph, weights cold:
+//   rows                              24         32         48         64
+//   16 bits gated, 4096 -> 8192       31.2/29.0  33.9/30.2  40.2/38.8  46.8/41.3
+//   16 bits gated, 2048 -> 5464       15.4/14.2  16.5/14.9  20.8/19.8  24.1/21.1
+//   16 bits gated, 8192 -> 1024       30.5/40.8  31.7/43.4  38.2/62.0  41.7/66.9
+//   4-bit gated, 8192 -> 16384        29.2/27.8  30.0/28.0  38.4/30.4  40.0/31.2
+//   4-bit gated, 4096 -> 8192         9.6/10.7   10.0/10.9  11.6/12.4  12.2/12.5
+//   4-bit gated, 8192 -> 1024         8.2/9.9    8.3/10.5   9.8/13.9   9.9/14.2
+//   4-bit product, 16384 -> 16384     28.3/29.6  29.7/30.3  38.8/32.4  38.8/33.0
+//   4-bit product, 4096 -> 16384      9.4/10.3   9.8/10.5   13.8/12.1  14.6/12.6
+//   4-bit product, 8192 -> 1024       7.5/10.1   7.8/10.5   9.4/12.7   10.1/13.7
+// What decides is the number of workgroups more than the type. The rule by type avoids
+// the largest loss of the other choice (16 bits 66.9 against 41.7, 4 bits 40.0 against
+// 31.2) and costs up to a seventh on wide 16-bit blocks, two fifths on narrow 4-bit ones.
 template <int DT, int EPI>
 hipError_t launch_skinny(const TileArgs& p, hipStream_t s) {
   constexpr int kWide = DT == kMX4 ? 4 : 2;

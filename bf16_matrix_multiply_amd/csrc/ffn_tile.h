@@ -51,13 +51,13 @@
 // of the slab before. The loop runs whole turns of the ring: slabs past the end
 // read as zeros.
 //
-// Measured on MI355X, 8192 x 4096 -> 8192 bf16: gated 746 us = 1474 TFLOP/s (the
-// library's plain 8192^3 product, as many operations, 663-689 us), of which 680 us
-// are the slab loops; dX and dW of its backward pass 760 us each; 8192^3 with
-// 4-bit operands 237 us = 4.6 PFLOP/s. Bound by the matrix cores at the clock that
-// the power limit leaves (bf16, 1.7-1.8 GHz), and by the LDS, whose reads and loads
-// leave bubbles between the MFMAs of the one wave that a SIMD has room for (4 bits:
-// without them 169 us). Tried and slower or no faster: reads and loads in bursts
+// Measured on MI355X, 8192 x 4096 -> 8192 bf16: gated 746-781 us = 1408-1474 TFLOP/s
+// from box to box (the library's plain 8192^3 product, as many operations, 663-707
+// us), of which 680 us are the slab loops; dX and dW of its backward pass 760-790 us
+// each; 8192^3 with 4-bit operands 237 us = 4.6 PFLOP/s. Bound by the matrix cores
+// at the clock that the power limit leaves (bf16, 1.7-1.8 GHz), and by the LDS, whose
+// reads and loads leave bubbles between the MFMAs of the one wave that a SIMD has
+// room for (4 bits: without them 169 us). Tried and slower or no faster: reads and loads in bursts
 // (820 -> 1000-1500 us), workgroups that go on to the next tile, a copy of the loop
 // for each wave with its reads and loads shifted, one barrier for two slabs, and
 // for 4 bits 32 x 32 x 64 MFMAs.

@@ -60,8 +60,9 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
 }
 
 // The largest finite magnitude of dG and dU that each workgroup meets, as float32
-// bits (which are ordered like the values). Bound by memory: 8192 x 8192 79 us = 5.1 TB/s;
-// of the whole backward pass 45 x 528 -> 1368 3 of 25 us, 32773 x 512 -> 1024 45 of 238.
+// bits (which are ordered like the values). Bound by memory: 8192 x 8192 72-79 us = 5.1-5.6
+// TB/s; of the whole backward pass 45 x 528 -> 1368 3 of 26 us, 32773 x 512 -> 1024
+// 37-45 of 238.
 template <int DT, int ACT>
 __global__ __launch_bounds__(kThreads) void peaks_kernel(uint32_t* __restrict__ peaks,
                                                          const uint16_t* __restrict__ dh,
@@ -238,6 +239,12 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
 // 128, 256 x 192 and 256 x 256: 777 rows 45.5, 52.3, 39.0 and 43.2 us, 1500 rows
 // 70, 83, 77 and 92, 4095 rows 163, 172, 164 and 148; the weight gradients of 32773
 // x 512 -> 1024 by 128 x 128 tiles 258 us, by 256 x 128 tiles and 8 splits 72.
+// Outside of those products it is rougher. Below 128 rows it expects too little (96
+// x 4096 -> 8192: 38 us, measured 45), without a worse choice. It does not know that a
+// gated call keeps its projections: where the sum is short, 128 x 128 tiles are then
+// often the better ones (kept, 4096 x 256 -> 4096: 47 us, chosen 256 x 256 56; 16384 x
+// 256 -> 2048: 83, chosen 97; but 8192 x 256 -> 8192: 230, chosen 159), and 256 x 192
+// tiles, which write the last columns in pieces of 32 bytes, the slowest (369 there).
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
   struct Size {
     int64_t tm, tn, places;
@@ -266,8 +273,18 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
   return best;
 }
 
-// Few rows: the weights are read once for up to 64 rows. Gated 4096 -> 8192 bf16:
-// 64 rows 43-46 us against 50 by 128 x 128 tiles, 96 rows 67 against 51.
+// Few rows: the weights are read once for up to 64 rows. Few-rows kernel / 128 x 128
+// tiles, the better of the others (us, launches from a graph, weights cold):
+//   rows                             33         48         64         65         128
+//   gated 4096 -> 8192, 16 bits      34.2/43.1  41.0/43.1  47.8/43.5  66.7/43.9  88.3/46.6
+//   gated 2048 -> 5464, 16 bits      18.0/21.7  21.2/21.8  24.4/21.9  29.6/21.9  34.7/22.7
+//   gated 8192 -> 1024, 16 bits      35.4/69.6  38.7/69.6  41.8/69.9  40.9/70.0  41.2/73.1
+//   gated 4096 -> 512, 16 bits       18.9/27.7  20.3/27.7  22.3/27.7  21.3/27.7  21.8/28.0
+//   gated 4096 -> 8192, 4 bits       12.8/13.6  12.9/13.6  13.0/13.7  17.3/13.8  18.0/14.3
+//   gated 8192 -> 1024, 4 bits       13.9/18.4  13.9/18.5  14.0/18.6  13.0/18.5  13.6/18.7
+//   product 16384 -> 16384, 4 bits   33.1/47.6  33.5/42.3  33.4/43.1  57.1/43.3  61.6/46.4
+// One limit for all: a wide 16-bit block would change at 56 rows (a tenth at 64), and a
+// narrow one, whose tiles leave most of the chip empty, not before 256.
 int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs) {
   if (M <= 64 && batch <= 65535) return kSkinny;
   return plan_tiles(batch, M, N, slabs, false).tile;
