@@ -31,7 +31,10 @@ __all__ = ["BmmError", "pack_operand", "pack_operand_kmajor", "box_copy", "box_s
            "splitk_workspace_bytes", "select_kernel", "library_path", "KERNELS", "MmaOpts",
            "ELEM_TYPES", "ACTS", "gated", "gated_backward", "gated_backward_workspace_bytes",
            "ffn_plan", "FFN_PRODUCTS", "FFN_TILES", "Mx4Operand", "mx4_quantize", "mx4_dequantize",
-           "mx4_mma", "mx4_gated"]
+           "mx4_mma", "mx4_gated", "grouped_mma", "grouped_mma_backward",
+           "grouped_mma_backward_workspace_bytes", "grouped_gated", "grouped_gated_backward",
+           "grouped_gated_backward_workspace_bytes", "I8Operand", "i8_quantize", "i8_pack",
+           "i8_mma", "i8_gated", "group_plan", "GROUP_PRODUCTS"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libbmm.so")
@@ -46,6 +49,8 @@ ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 FFN_PRODUCTS = {"gated": 0, "gated_dx": 1, "gated_dx_rest": 2, "gated_dw": 3, "mx4_mma": 4,
                 "mx4_gated": 5}
 FFN_TILES = {"128x128": 0, "256x128": 1, "256x192": 2, "256x256": 3, "few_rows": 4, "none": 5}
+GROUP_PRODUCTS = {"grouped_mma": 0, "grouped_mma_dx": 1, "grouped_mma_dw": 2, "grouped_gated": 3,
+                  "grouped_gated_dx": 4, "grouped_gated_dw": 5, "i8_mma": 6, "i8_gated": 7}
 _HALF_DTYPES = {torch.float16: BMM_F16, torch.bfloat16: BMM_BF16}
 _ELEM_DTYPES = {torch.float32: 1, torch.float16: 2, torch.bfloat16: 3}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
@@ -93,6 +98,34 @@ class GatedDesc(ctypes.Structure):
         ("ld_h", ctypes.c_int64),
         ("dtype", ctypes.c_int32),
         ("act", ctypes.c_int32),
+    ]
+
+
+class GroupedDesc(ctypes.Structure):
+    _fields_ = [
+        ("groups", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("ld_x", ctypes.c_int64),
+        ("ld_y", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("zero_tail", ctypes.c_int32),
+    ]
+
+
+class I8Desc(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64),
+        ("M", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("ld_a", ctypes.c_int64),
+        ("ld_d", ctypes.c_int64),
+        ("elem_type", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+        ("zero_tail", ctypes.c_int32),
     ]
 
 
@@ -162,6 +195,23 @@ def lib():
         L.bmm_ffn_plan.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(i32)]
         for f in (L.bmm_ffn_plan, L.bmm_gated, L.bmm_gated_backward, L.bmm_mx4_quantize,
                   L.bmm_mx4_dequantize, L.bmm_mx4_mma, L.bmm_mx4_gated):
+            f.restype = ctypes.c_int
+        desc, i8 = ctypes.POINTER(GroupedDesc), ctypes.POINTER(I8Desc)
+        L.bmm_grouped_mma.argtypes = [p] * 4 + [desc, p]
+        L.bmm_grouped_mma_backward.argtypes = [p] * 6 + [desc, p, i64, p]
+        L.bmm_grouped_gated.argtypes = [p] * 7 + [desc, p]
+        L.bmm_grouped_gated_backward.argtypes = [p] * 10 + [desc, p, i64, p]
+        for f in (L.bmm_grouped_mma_backward_workspace_bytes,
+                  L.bmm_grouped_gated_backward_workspace_bytes):
+            f.argtypes = [desc]
+            f.restype = i64
+        L.bmm_i8_quantize.argtypes = [p, p, p, i64, i64, i64, i64, i32, p]
+        L.bmm_i8_mma.argtypes = [p] * 6 + [i8, p]
+        L.bmm_i8_gated.argtypes = [p] * 8 + [i8, p]
+        L.bmm_group_plan.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(i32)]
+        for f in (L.bmm_grouped_mma, L.bmm_grouped_mma_backward, L.bmm_grouped_gated,
+                  L.bmm_grouped_gated_backward, L.bmm_i8_quantize, L.bmm_i8_mma, L.bmm_i8_gated,
+                  L.bmm_group_plan):
             f.restype = ctypes.c_int
         _lib = L
     return _lib
@@ -836,3 +886,352 @@ def mx4_gated(X: Mx4Operand, Wg: Mx4Operand, Wu: Mx4Operand, act: str = "silu",
     if rc < 0:
         _check(rc)
     return out
+
+
+# ---- products by groups of rows (the experts of a mixture) ----
+
+def _group_weights(ws, names, ends, K, fn):
+    """(groups, N) of packed weights (groups, N/8, K/16, 8, 8) and their row ends."""
+    shape = ws[0].shape
+    if ends.dtype != torch.int32 or ends.dim() != 1 or not ends.is_contiguous():
+        raise ValueError(f"{fn}: ends must be a contiguous int32 tensor of one dimension")
+    for w, name in zip(ws, names):
+        if w.dim() != 5 or w.shape[3:] != (8, 8) or w.element_size() != 4 or not w.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be contiguous packed words (groups, N/8, K/16, 8, 8) "
+                             "(pack_operand with atom_rows 8)")
+        if w.shape != shape:
+            raise ValueError(f"{fn}: {names[0]} and {name} differ in shape")
+    if shape[0] != ends.shape[0]:
+        raise ValueError(f"{fn}: {ends.shape[0]} ends for the weights of {shape[0]} groups")
+    if K != 16 * shape[2]:
+        raise ValueError(f"{fn}: X and the weights disagree on K")
+    return shape[0], 8 * shape[1]
+
+
+def _group_rows(X, name, fn):
+    """(element type, row stride) of a (T, K) matrix."""
+    if X.dim() != 2:
+        raise ValueError(f"{fn}: {name} must be (rows, columns), all groups' rows one after another")
+    return _half_matrix(X, name, fn), _rows_ld(X, name, fn)
+
+
+def grouped_mma(X: torch.Tensor, W: torch.Tensor, ends: torch.Tensor,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = X W_e^T for the rows of each group e (bmm_grouped_mma): the rows of each
+    expert of a mixture with its own weight, in one kernel.
+
+    X is (T, K) float16 or bfloat16, its rows sorted by group, any multiple of 8
+    elements apart; W is (E, N/8, K/16, 8, 8) packed words (pack_operand(w, 8) of
+    (E, N, K)) of the same type. ``ends`` is (E,) int32 on the same GPU: group e has
+    the rows from ends[e - 1] (the first from 0) up to ends[e], the running sum of
+    the groups' sizes; the host does not read it. Rows behind the last group are
+    not read; their outputs are zero, or with ``out`` given left as they were.
+    Returns Y (T, N) in X's type."""
+    fn = "grouped_mma"
+    device = X.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, grouped_mma, X, W, ends, out)
+    if not (out is None and 0 <= device == W.get_device() == ends.get_device()):
+        _require_cuda(X, W, ends, out)
+    dt, ld_x = _group_rows(X, "X", fn)
+    T, K = X.shape
+    E, N = _group_weights((W,), ("W",), ends, K, fn)
+    Y, ld_y = _out(out, (T, N), X.dtype, X, fn)
+    d = GroupedDesc(E, T, N, K, ld_x, ld_y, dt, 0, out is None)
+    rc = (_lib or lib()).bmm_grouped_mma(Y.data_ptr(), X.data_ptr(), W.data_ptr(), ends.data_ptr(),
+                                         ctypes.byref(d), _current_stream(device))
+    if rc < 0:
+        _check(rc)
+    return Y
+
+
+def grouped_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, ends: torch.Tensor,
+                  act: str = "silu", save: bool = False, out: torch.Tensor | None = None):
+    """H = act(X Wg_e^T) * (X Wu_e^T) for the rows of each group e (bmm_grouped_gated).
+
+    X, the weights and ``ends`` as in grouped_mma. Returns H (T, F) in X's type, and
+    with ``save`` (H, G, U), the projections that grouped_gated_backward takes."""
+    fn = "grouped_gated"
+    code = _act_code(act, fn)
+    device = X.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, grouped_gated, X, Wg, Wu, ends, act, save, out)
+    if not (out is None and 0 <= device == Wg.get_device() == Wu.get_device() == ends.get_device()):
+        _require_cuda(X, Wg, Wu, ends, out)
+    dt, ld_x = _group_rows(X, "X", fn)
+    T, K = X.shape
+    E, F = _group_weights((Wg, Wu), ("Wg", "Wu"), ends, K, fn)
+    H, ld_h = _out(out, (T, F), X.dtype, X, fn)
+    G = U = None
+    if save:
+        if ld_h != F and H.numel():
+            raise ValueError(f"{fn}: with save, out must be contiguous")
+        # (with out given its rows behind the last group stay, and G and U have no old ones)
+        new = X.new_empty if out is None else X.new_zeros
+        G, U = new((T, F)), new((T, F))
+    d = GroupedDesc(E, T, F, K, ld_x, ld_h, dt, code, out is None)
+    rc = (_lib or lib()).bmm_grouped_gated(H.data_ptr(), _addr(G), _addr(U), X.data_ptr(),
+                                           Wg.data_ptr(), Wu.data_ptr(), ends.data_ptr(),
+                                           ctypes.byref(d), _current_stream(device))
+    if rc < 0:
+        _check(rc)
+    return (H, G, U) if save else H
+
+
+def grouped_mma_backward_workspace_bytes(groups: int, T: int, N: int, K: int) -> int:
+    """bmm_grouped_mma_backward_workspace_bytes for these extents."""
+    d = GroupedDesc(groups, T, N, K, K, N, BMM_BF16, 0, 1)
+    return _check(lib().bmm_grouped_mma_backward_workspace_bytes(ctypes.byref(d)))
+
+
+def grouped_gated_backward_workspace_bytes(groups: int, T: int, F: int, K: int) -> int:
+    """bmm_grouped_gated_backward_workspace_bytes for these extents."""
+    d = GroupedDesc(groups, T, F, K, K, F, BMM_BF16, 0, 1)
+    return _check(lib().bmm_grouped_gated_backward_workspace_bytes(ctypes.byref(d)))
+
+
+def _grad_workspace(need, workspace, X, fn):
+    if workspace is None:
+        return X.new_empty(need, dtype=torch.uint8)
+    if not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    return workspace
+
+
+def _same_rows(ts, names, shape, dtype, fn) -> int:
+    """The common row stride of matrices of one shape and type."""
+    ld = None
+    for t, name in zip(ts, names):
+        if t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{fn}: {name} must be a {dtype} tensor of shape {shape}")
+        own = _rows_ld(t, name, fn)
+        if ld is not None and own != ld:
+            raise ValueError(f"{fn}: {', '.join(names)} must have the same row stride")
+        ld = own
+    return ld
+
+
+@_on_its_gpu
+def grouped_mma_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, ends: torch.Tensor,
+                         need_dx: bool = True, need_dw: bool = True,
+                         workspace: torch.Tensor | None = None):
+    """Gradients of grouped_mma (bmm_grouped_mma_backward): (dX, dW) for dY = dL/dY.
+
+    dX is (T, K), zero behind the last group; dW is row-major (E, N, K), zero for a
+    group without rows; both in X's type, None for what need_dx or need_dw leaves
+    out. ``workspace`` (any contiguous tensor of at least
+    grouped_mma_backward_workspace_bytes) is allocated here when not given."""
+    fn = "grouped_mma_backward"
+    if not (need_dx or need_dw):
+        raise ValueError(f"{fn}: neither need_dx nor need_dw")
+    _require_cuda(dY, X, W, ends, workspace)
+    dt, ld_x = _group_rows(X, "X", fn)
+    T, K = X.shape
+    E, N = _group_weights((W,), ("W",), ends, K, fn)
+    ld_y = _same_rows((dY,), ("dY",), (T, N), X.dtype, fn)
+    d = GroupedDesc(E, T, N, K, ld_x, ld_y, dt, 0, 1)
+    need = _check(lib().bmm_grouped_mma_backward_workspace_bytes(ctypes.byref(d)))
+    workspace = _grad_workspace(need, workspace, X, fn)
+    dX = X.new_empty((T, K)) if need_dx else None
+    dW = X.new_empty((E, N, K)) if need_dw else None
+    _check(lib().bmm_grouped_mma_backward(
+        _addr(dX), _addr(dW), _addr(dY), _addr(X), _addr(W), _addr(ends), ctypes.byref(d),
+        _addr(workspace), workspace.numel() * workspace.element_size(),
+        _current_stream(_current_device())))
+    return dX, dW
+
+
+@_on_its_gpu
+def grouped_gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, X: torch.Tensor,
+                           Wg: torch.Tensor, Wu: torch.Tensor, ends: torch.Tensor,
+                           act: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                           workspace: torch.Tensor | None = None):
+    """Gradients of grouped_gated (bmm_grouped_gated_backward): (dX, dWg, dWu) for dH
+    = dL/dH and the projections that grouped_gated(..., save=True) returned.
+
+    As grouped_mma_backward, with dWg and dWu (E, F, K) in dW's place. dH, G and U
+    share one row stride."""
+    fn = "grouped_gated_backward"
+    code = _act_code(act, fn)
+    if not (need_dx or need_dw):
+        raise ValueError(f"{fn}: neither need_dx nor need_dw")
+    _require_cuda(dH, G, U, X, Wg, Wu, ends, workspace)
+    dt, ld_x = _group_rows(X, "X", fn)
+    T, K = X.shape
+    E, F = _group_weights((Wg, Wu), ("Wg", "Wu"), ends, K, fn)
+    ld_h = _same_rows((dH, G, U), ("dH", "G", "U"), (T, F), X.dtype, fn)
+    d = GroupedDesc(E, T, F, K, ld_x, ld_h, dt, code, 1)
+    need = _check(lib().bmm_grouped_gated_backward_workspace_bytes(ctypes.byref(d)))
+    workspace = _grad_workspace(need, workspace, X, fn)
+    dX = X.new_empty((T, K)) if need_dx else None
+    dWg = dWu = None
+    if need_dw:
+        dWg, dWu = X.new_empty((E, F, K)), X.new_empty((E, F, K))
+    _check(lib().bmm_grouped_gated_backward(
+        _addr(dX), _addr(dWg), _addr(dWu), _addr(dH), _addr(G), _addr(U), _addr(X), _addr(Wg),
+        _addr(Wu), _addr(ends), ctypes.byref(d), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _current_stream(_current_device())))
+    return dX, dWg, dWu
+
+
+def group_plan(product: str, groups: int, T: int, N: int, K: int) -> tuple[str, int]:
+    """How a product by groups or of 8-bit integers is made (bmm_group_plan): its tile,
+    one of FFN_TILES, and the number of parts that its sum is cut into. ``product`` is
+    one of GROUP_PRODUCTS; N is the width F of a gated block; groups 0: one 8-bit
+    weight."""
+    splits = ctypes.c_int32()
+    tile = _check(lib().bmm_group_plan(GROUP_PRODUCTS[product], groups, T, N, K,
+                                       ctypes.byref(splits)))
+    return FFN_TILE_NAMES[tile], splits.value
+
+
+# ---- 8-bit integers ----
+
+class I8Operand(typing.NamedTuple):
+    """8-bit codes with a float32 scale for each row. As i8_quantize makes them:
+    codes (rows, K) or (batch, rows, K) int8, scales (rows,) or (batch, rows). As a
+    weight (i8_pack): codes (batch, rows/8, K/32, 8, 8) packed 32-bit words, scales
+    (batch, rows); by groups the batch is the groups."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+def i8_quantize(X: torch.Tensor) -> I8Operand:
+    """(rows, K) or (batch, rows, K) float32, float16 or bfloat16 to codes -127 .. 127
+    and a scale for each row, max |x| / 127 (bmm_i8_quantize). K is a multiple of 32;
+    rows may be any multiple of 8 elements apart."""
+    fn = "i8_quantize"
+    device = X.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, i8_quantize, X)
+    if not X.is_cuda:
+        _require_cuda(X)
+    elem = _ELEM_DTYPES.get(X.dtype)
+    if elem is None:
+        raise ValueError(f"{fn}: X must be float32, float16 or bfloat16, got {X.dtype}")
+    ld = _rows_ld(X, "X", fn)
+    *lead, rows, K = X.shape
+    codes = X.new_empty(X.shape, dtype=torch.int8)
+    scales = X.new_empty((*lead, rows), dtype=torch.float32)
+    rc = (_lib or lib()).bmm_i8_quantize(codes.data_ptr(), scales.data_ptr(), X.data_ptr(),
+                                         lead[0] if lead else 1, rows, K, ld, elem,
+                                         _current_stream(device))
+    if rc < 0:
+        _check(rc)
+    return I8Operand(codes, scales)
+
+
+def i8_pack(A: I8Operand) -> I8Operand:
+    """Row-major codes (rows, K) or (batch, rows, K) as a weight of i8_mma and
+    i8_gated (pack_operand of the codes, two as a 16-bit value). Rows are a multiple
+    of 8, K of 32."""
+    codes, scales = A
+    if codes.dtype != torch.int8 or codes.dim() not in (2, 3) or not codes.is_contiguous():
+        raise ValueError("i8_pack: codes must be contiguous int8 (rows, K) or (batch, rows, K)")
+    if codes.shape[:-1] != scales.shape:
+        raise ValueError("i8_pack: codes and scales disagree on the rows")
+    if codes.shape[-2] % 8 or codes.shape[-1] % 32:
+        raise ValueError("i8_pack: rows must be a multiple of 8 and K of 32")
+    return I8Operand(pack_operand(codes.view(torch.int16), 8),
+                     scales if scales.dim() == 2 else scales[None])
+
+
+def _i8_rows(A, name, fn):
+    """(row stride, batch) of a row-major operand."""
+    codes, scales = A
+    if codes.dtype != torch.int8:
+        raise ValueError(f"{fn}: {name}.codes must be int8, got {codes.dtype}")
+    shape, stride = codes.shape, codes.stride()
+    if scales.shape != shape[:-1] or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"{fn}: {name}.scales must be contiguous float32 of shape {tuple(shape[:-1])}")
+    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1 and shape[1] > 1:
+        return stride[0], 1
+    return _rows_ld(codes, f"{name}.codes", fn), shape[0] if len(shape) == 3 else 1
+
+
+def _i8_weight(B, name, K, fn):
+    """(batch, N) of a packed operand."""
+    codes, scales = B
+    shape = codes.shape
+    if codes.dim() != 5 or shape[3:] != (8, 8) or codes.element_size() != 4 \
+            or not codes.is_contiguous():
+        raise ValueError(f"{fn}: {name}.codes must be contiguous packed words (batch, N/8, K/32, 8, 8) "
+                         "(i8_pack)")
+    batch, N = shape[0], 8 * shape[1]
+    if scales.shape != (batch, N) or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"{fn}: {name}.scales must be contiguous float32 of shape {(batch, N)}")
+    if K != 32 * shape[2]:
+        raise ValueError(f"{fn}: the operands disagree on K")
+    return batch, N
+
+
+def _i8_desc(A, ws, names, ends, dtype, act, out, fn):
+    """(output, descriptor) of a product of a row-major operand and packed weights."""
+    ld_a, batch = _i8_rows(A, names[0], fn)
+    shape = A.codes.shape
+    M, K = shape[-2:]
+    batch_w, N = _i8_weight(ws[0], names[1], K, fn)
+    if len(ws) == 2 and _i8_weight(ws[1], names[2], K, fn) != (batch_w, N):
+        raise ValueError(f"{fn}: {names[1]} and {names[2]} differ in shape")
+    if ends is None:
+        if batch != batch_w:
+            raise ValueError(f"{fn}: {names[0]} and {names[1]} disagree on batch")
+    else:
+        if len(shape) != 2:
+            raise ValueError(f"{fn}: with ends, {names[0]} must be (rows, K)")
+        if ends.dtype != torch.int32 or ends.dim() != 1 or not ends.is_contiguous():
+            raise ValueError(f"{fn}: ends must be a contiguous int32 tensor of one dimension")
+        if ends.shape[0] != batch_w:
+            raise ValueError(f"{fn}: {ends.shape[0]} ends for the weights of {batch_w} groups")
+    D, ld_d = _out(out, (*shape[:-1], N), dtype, A.codes, fn)
+    return D, I8Desc(batch_w, M, N, K, ld_a, ld_d, _ELEM_DTYPES[dtype], act, out is None)
+
+
+def i8_mma(A: I8Operand, B: I8Operand, ends: torch.Tensor | None = None,
+           dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """D = A B^T of 8-bit integers with a scale for each row of both (bmm_i8_mma):
+    (M, N) or (batch, M, N) in ``dtype`` (float32, float16 or bfloat16).
+
+    A is row-major (i8_quantize), B packed (i8_pack of an i8_quantize, or a
+    checkpoint's codes). With ``ends`` the rows of A are sorted by group and B holds
+    a weight for each, as in grouped_mma."""
+    fn = "i8_mma"
+    a, sa = A
+    b, sb = B
+    device = a.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, i8_mma, A, B, ends, dtype, out)
+    _require_cuda(a, sa, b, sb, ends, out)
+    if dtype not in _ELEM_DTYPES:
+        raise ValueError(f"{fn}: dtype must be float32, float16 or bfloat16, got {dtype}")
+    D, d = _i8_desc(A, (B,), ("A", "B"), ends, dtype, 0, out, fn)
+    rc = (_lib or lib()).bmm_i8_mma(D.data_ptr(), a.data_ptr(), sa.data_ptr(), b.data_ptr(),
+                                    sb.data_ptr(), _addr(ends), ctypes.byref(d),
+                                    _current_stream(device))
+    if rc < 0:
+        _check(rc)
+    return D
+
+
+def i8_gated(X: I8Operand, Wg: I8Operand, Wu: I8Operand, ends: torch.Tensor | None = None,
+             act: str = "silu", dtype: torch.dtype = torch.bfloat16,
+             out: torch.Tensor | None = None) -> torch.Tensor:
+    """H = act(X Wg^T) * (X Wu^T) over 8-bit integers (bmm_i8_gated): (M, F) or (batch,
+    M, F) in ``dtype`` (float16 or bfloat16). Operands and ``ends`` as in i8_mma."""
+    fn = "i8_gated"
+    code = _act_code(act, fn)
+    x, sx = X
+    device = x.get_device()
+    if device >= 0 and device != _current_device():
+        return _on_gpu(device, i8_gated, X, Wg, Wu, ends, act, dtype, out)
+    _require_cuda(x, sx, *Wg, *Wu, ends, out)
+    if dtype not in _HALF_DTYPES:
+        raise ValueError(f"{fn}: dtype must be float16 or bfloat16, got {dtype}")
+    H, d = _i8_desc(X, (Wg, Wu), ("X", "Wg", "Wu"), ends, dtype, code, out, fn)
+    rc = (_lib or lib()).bmm_i8_gated(H.data_ptr(), x.data_ptr(), sx.data_ptr(),
+                                      Wg.codes.data_ptr(), Wg.scales.data_ptr(),
+                                      Wu.codes.data_ptr(), Wu.scales.data_ptr(), _addr(ends),
+                                      ctypes.byref(d), _current_stream(device))
+    if rc < 0:
+        _check(rc)
+    return H

@@ -1,38 +1,8 @@
 // extern "C" entry points of the feed-forward operators (include/bmm.h):
 // validate on the host, then enqueue the kernels on the caller's stream.
-#include <exception>
-#include <string>
-
-#include "ffn.h"
-#include "validate.h"
+#include "abi_util.h"
 
 namespace {
-
-int report(const bmm::Status& st) {
-  bmm::set_last_error(st.msg);
-  return st.code;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return report(bmm::Status{});
-  bmm::set_last_error(std::string(what) + ": " + hipGetErrorString(e));
-  return BMM_EHIP;
-}
-
-// No exception (out of host memory in a message, say) leaves a C entry point.
-template <class Fn>
-auto guarded(Fn fn) noexcept -> decltype(fn()) {
-  try {
-    return fn();
-  } catch (...) {
-    return BMM_EHIP;
-  }
-}
-
-// Start of the second block of output rows where there is none.
-constexpr int64_t kNoRow = int64_t(1) << 62;
-
-int64_t padded_width(int64_t F) { return (F + 31) / 32 * 32; }
 
 // Layout of the backward pass's workspace: [dG | dU], the factor that undoes their
 // scaling and the peaks that it comes from (f16; kept for both types, so that a
@@ -51,7 +21,7 @@ constexpr double kLaunchNs = 4000;
 
 BackwardPlan plan_backward(const bmm_gated_desc& d) {
   BackwardPlan p;
-  const int64_t Fp2 = 2 * padded_width(d.F);
+  const int64_t Fp2 = 2 * bmm::padded_width(d.F);
   p.dgu_bytes = d.batch * d.M * Fp2 * 2;
   const int64_t peaks = bmm::gated_peaks(d.batch * d.M, d.F);
   p.slopes_bytes = (p.dgu_bytes + (peaks > 0 ? 4 * (1 + peaks) : 0) + 255) / 256 * 256;
@@ -104,11 +74,11 @@ extern "C" {
 
 int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const uint32_t* Wg,
               const uint32_t* Wu, const bmm_gated_desc* desc, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bmm::Status st = bmm::check_gated(H, G, U, X, Wg, Wu, desc);
-    if (!st.ok()) return report(st);
+    if (!st.ok()) return bmm::report(st);
     const bmm_gated_desc& d = *desc;
-    if (d.batch == 0 || d.M == 0 || d.F == 0) return report(st);
+    if (d.batch == 0 || d.M == 0 || d.F == 0) return bmm::report(st);
     bmm::TileArgs a = gated_args(d);
     a.a = X;
     a.b0 = Wg;
@@ -124,15 +94,15 @@ int bmm_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const ui
     a.a_bs = d.M * d.ld_x;
     a.b_bs = d.F * d.K;
     a.tile = gated_tile(d);
-    return hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
+    return bmm::hip_status(bmm::launch_gated(a, d.dtype, static_cast<hipStream_t>(stream)),
                       "gated launch");
   });
 }
 
 int64_t bmm_gated_backward_workspace_bytes(const bmm_gated_desc* desc) {
-  return guarded([&]() -> int64_t {
+  return bmm::guarded([&]() -> int64_t {
     const bmm::Status st = bmm::check_gated_desc(desc, "gated_backward");
-    if (!st.ok()) return report(st);
+    if (!st.ok()) return bmm::report(st);
     return plan_backward(*desc).need;
   });
 }
@@ -141,28 +111,28 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
                        const uint16_t* G, const uint16_t* U, const uint16_t* X,
                        const uint32_t* Wg, const uint32_t* Wu, const bmm_gated_desc* desc,
                        void* workspace, int64_t workspace_bytes, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     bmm::Status st = bmm::check_gated_desc(desc, "gated_backward");
-    if (!st.ok()) return report(st);
+    if (!st.ok()) return bmm::report(st);
     const bmm_gated_desc& d = *desc;
     const BackwardPlan plan = plan_backward(d);
     st = bmm::check_gated_backward(dX, dWg, dWu, dH, G, U, X, Wg, Wu, desc, workspace,
                                    workspace_bytes, plan.need);
-    if (!st.ok()) return report(st);
-    if (d.batch == 0 || d.K == 0 || (d.M == 0 && d.F == 0)) return report(st);
+    if (!st.ok()) return bmm::report(st);
+    if (d.batch == 0 || d.K == 0 || (d.M == 0 && d.F == 0)) return bmm::report(st);
     hipStream_t s = static_cast<hipStream_t>(stream);
     uint16_t* const dgu = static_cast<uint16_t*>(workspace);
     float* const part =
         reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.slopes_bytes);
-    const int64_t Fp = padded_width(d.F);
+    const int64_t Fp = bmm::padded_width(d.F);
     float* rescale = nullptr;   // (no [dG | dU]: no factor either)
     uint32_t* peaks = nullptr;
     if (plan.dgu_bytes > 0) {
       rescale = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.dgu_bytes);
       peaks = reinterpret_cast<uint32_t*>(rescale + 1);
     }
-    int rc = hip_status(bmm::launch_gated_slopes(dgu, dH, G, U, d.batch * d.M, d.F, d.ld_h,
-                                                 d.dtype, d.act, peaks, rescale, s),
+    int rc = bmm::hip_status(bmm::launch_gated_slopes(dgu, dH, G, U, d.batch * d.M, d.F, d.ld_h,
+                                                 d.dtype, d.act, nullptr, peaks, rescale, s),
                         "gated_backward slopes launch");
     if (rc != BMM_OK) return rc;
     auto rows_of_dx = [&](int64_t row, int64_t rows, const bmm::TilePlan& tiles) {
@@ -172,7 +142,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.b1 = Wu;
       a.d = dX + row * d.K;
       a.M = a.rows0 = rows;
-      a.row1 = kNoRow;
+      a.row1 = bmm::kNoRow;
       a.N = a.ldd = d.K;
       a.K = a.lda = 2 * Fp;
       a.a_bs = d.M * 2 * Fp;
@@ -184,7 +154,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.part = part;
       a.part_floats = d.batch * rows * d.K;
       a.rescale = rescale;
-      return hip_status(bmm::launch_gated_dx(a, d.dtype, s), "gated_backward dX launch");
+      return bmm::hip_status(bmm::launch_gated_dx(a, d.dtype, s), "gated_backward dX launch");
     };
     if (dX && d.M > 0) {
       rc = rows_of_dx(0, plan.dx_rows, plan.dx);
@@ -211,7 +181,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       a.part = part;
       a.part_floats = d.batch * 2 * Fp * d.K;
       a.rescale = rescale;
-      rc = hip_status(bmm::launch_gated_dw(a, d.dtype, s), "gated_backward dW launch");
+      rc = bmm::hip_status(bmm::launch_gated_dw(a, d.dtype, s), "gated_backward dW launch");
     }
     return rc;
   });
@@ -219,11 +189,11 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
 
 int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K,
                  int32_t* splits) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bool four = product == BMM_FFN_MX4_MMA || product == BMM_FFN_MX4_GATED;
     const bmm_gated_desc d{batch, M, F, K, K, F, BMM_BF16, BMM_ACT_SILU};
     const bmm::Status st = bmm::check_ffn_plan(product, d);
-    if (!st.ok()) return report(st);
+    if (!st.ok()) return bmm::report(st);
     bmm::TilePlan plan{BMM_TILE_NONE, 1, 0};
     // (the backward pass writes the zeros of an empty sum: dX for F = 0, dWg and dWu for M = 0)
     const bool forward = four || product == BMM_FFN_GATED, dw = product == BMM_FFN_GATED_DW;
@@ -240,7 +210,7 @@ int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K
       else if (b.dx_rows < M) plan = b.dx_rest;
     }
     if (splits) *splits = plan.splits;
-    report(st);
+    bmm::report(st);
     return plan.tile;
   });
 }
@@ -257,12 +227,12 @@ int64_t bmm_mx4_scales_bytes(int64_t batch, int64_t rows, int64_t K) {
 
 int bmm_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t batch, int64_t rows,
                      int64_t K, int64_t ld_src, int32_t elem_type, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bmm::Status st = bmm::check_mx4_convert(src, codes, scales, batch, rows, K, ld_src,
                                                   elem_type, "mx4_quantize");
-    if (!st.ok()) return report(st);
-    if (batch == 0 || rows == 0 || K == 0) return report(st);
-    return hip_status(bmm::launch_mx4_quantize(codes, scales, src, batch, rows, K, ld_src,
+    if (!st.ok()) return bmm::report(st);
+    if (batch == 0 || rows == 0 || K == 0) return bmm::report(st);
+    return bmm::hip_status(bmm::launch_mx4_quantize(codes, scales, src, batch, rows, K, ld_src,
                                                elem_type, static_cast<hipStream_t>(stream)),
                       "mx4_quantize launch");
   });
@@ -270,12 +240,12 @@ int bmm_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t b
 
 int bmm_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales, int64_t batch,
                        int64_t rows, int64_t K, int64_t ld_dst, int32_t elem_type, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bmm::Status st = bmm::check_mx4_convert(dst, codes, scales, batch, rows, K, ld_dst,
                                                   elem_type, "mx4_dequantize");
-    if (!st.ok()) return report(st);
-    if (batch == 0 || rows == 0 || K == 0) return report(st);
-    return hip_status(bmm::launch_mx4_dequantize(dst, codes, scales, batch, rows, K, ld_dst,
+    if (!st.ok()) return bmm::report(st);
+    if (batch == 0 || rows == 0 || K == 0) return bmm::report(st);
+    return bmm::hip_status(bmm::launch_mx4_dequantize(dst, codes, scales, batch, rows, K, ld_dst,
                                                  elem_type, static_cast<hipStream_t>(stream)),
                       "mx4_dequantize launch");
   });
@@ -284,12 +254,12 @@ int bmm_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales, i
 int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const uint8_t* B_codes,
                 const uint8_t* B_scales, int64_t batch, int64_t M, int64_t N, int64_t K,
                 int64_t ld_d, int32_t elem_type, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bmm::Status st =
         bmm::check_mx4_product(D, A_codes, A_scales, B_codes, B_scales, nullptr, nullptr, false,
                                batch, M, N, K, ld_d, 0, elem_type);
-    if (!st.ok()) return report(st);
-    if (batch == 0 || M == 0 || N == 0) return report(st);
+    if (!st.ok()) return bmm::report(st);
+    if (batch == 0 || M == 0 || N == 0) return bmm::report(st);
     bmm::TileArgs a{};
     a.a = A_codes;
     a.as = A_scales;
@@ -298,7 +268,7 @@ int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const 
     a.d = D;
     a.batch = batch;
     a.M = a.rows0 = M;
-    a.row1 = kNoRow;
+    a.row1 = bmm::kNoRow;
     a.N = N;
     a.K = K;
     a.ldd = ld_d;
@@ -309,7 +279,7 @@ int bmm_mx4_mma(void* D, const uint8_t* A_codes, const uint8_t* A_scales, const 
     a.out_type = elem_type;
     a.splits = 1;
     a.tile = mx4_tile(batch, M, N, K);
-    return hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
+    return bmm::hip_status(bmm::launch_mx4_mma(a, static_cast<hipStream_t>(stream)), "mx4_mma launch");
   });
 }
 
@@ -317,12 +287,12 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
                   const uint8_t* Wg_codes, const uint8_t* Wg_scales, const uint8_t* Wu_codes,
                   const uint8_t* Wu_scales, int64_t batch, int64_t M, int64_t F, int64_t K,
                   int64_t ld_h, int32_t act, int32_t elem_type, void* stream) {
-  return guarded([&] {
+  return bmm::guarded([&] {
     const bmm::Status st =
         bmm::check_mx4_product(H, X_codes, X_scales, Wg_codes, Wg_scales, Wu_codes, Wu_scales,
                                true, batch, M, F, K, ld_h, act, elem_type);
-    if (!st.ok()) return report(st);
-    if (batch == 0 || M == 0 || F == 0) return report(st);
+    if (!st.ok()) return bmm::report(st);
+    if (batch == 0 || M == 0 || F == 0) return bmm::report(st);
     bmm::TileArgs a{};
     a.a = X_codes;
     a.as = X_scales;
@@ -344,7 +314,7 @@ int bmm_mx4_gated(void* H, const uint8_t* X_codes, const uint8_t* X_scales,
     a.out_type = elem_type;
     a.splits = 1;
     a.tile = mx4_tile(batch, M, 2 * F, K);
-    return hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
+    return bmm::hip_status(bmm::launch_mx4_gated(a, static_cast<hipStream_t>(stream)),
                       "mx4_gated launch");
   });
 }

@@ -11,9 +11,14 @@
 
 namespace bmm {
 
-// Operand element of a product: kF16 and kBF16 of common.h, or 4-bit floats
-// with a scale for every 32 K values.
-enum : int { kMX4 = 2 };
+// Operand element of a product: kF16 and kBF16 of common.h, 4-bit floats with a
+// scale for every 32 K values, or 8-bit integers with a scale for every row. Two
+// 8-bit integers count as one 16-bit value wherever operands are addressed: their
+// layouts are those of the 16-bit types with half the K.
+enum : int { kMX4 = 2, kI8 = 3 };
+
+// Types whose results may be rounded to any output type.
+constexpr bool any_output(int dt) { return dt == kMX4 || dt == kI8; }
 
 // How a product is made: by tiles of so many rows x columns (gated: columns of
 // both weights), or by the kernel for few rows (ffn_skinny.h).
@@ -55,6 +60,13 @@ struct TileArgs {
   float* part;
   int64_t part_floats;
   const float* rescale;     // f16 store: the sums are multiplied by this power of two (null: 1)
+  // groups (ffn_groups.h): `batch` groups of the M (weight gradients: K) rows
+  const int32_t* ends;
+  int zero_tail;            // whether rows of D behind the last group become zero
+  // 8-bit integers: scales of A's rows and of the rows of b0 and b1
+  const float* sa;
+  const float* sb0;
+  const float* sb1;
 };
 
 // ---- launchers ----
@@ -66,9 +78,20 @@ hipError_t launch_gated(const TileArgs& a, int dtype, hipStream_t s);
 int64_t gated_peaks(int64_t rows, int64_t F);
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, uint32_t* peaks, float* rescale, hipStream_t s);
+                               int act, const int32_t* end, uint32_t* peaks, float* rescale,
+                               hipStream_t s);   // end: rows from *end on are not made (null: all)
 hipError_t launch_gated_dx(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s);
+// By groups of rows (ffn_groups.h).
+hipError_t launch_grouped_mma(const TileArgs& a, int dtype, hipStream_t s);
+hipError_t launch_grouped_gated(const TileArgs& a, int dtype, hipStream_t s);
+hipError_t launch_grouped_dx(const TileArgs& a, int dtype, hipStream_t s);
+hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s);
+hipError_t launch_i8_quantize(int8_t* codes, float* scales, const void* src, int64_t rows, int64_t K,
+                              int64_t ld, int elem_type, hipStream_t s);
+// a.ends: by groups, or null.
+hipError_t launch_i8_mma(const TileArgs& a, hipStream_t s);
+hipError_t launch_i8_gated(const TileArgs& a, hipStream_t s);
 hipError_t launch_mx4_quantize(uint8_t* codes, uint8_t* scales, const void* src, int64_t batch,
                                int64_t rows, int64_t K, int64_t ld, int elem_type, hipStream_t s);
 hipError_t launch_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t* scales,
@@ -85,6 +108,9 @@ struct TilePlan {
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split);
 // The same for a product that has the kernel for few rows and no splits.
 int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs);
+// By E groups of T rows.
+TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool may_split);
+int plan_group_forward(int64_t E, int64_t T, int64_t N, int64_t slabs);
 
 // ---- activations ----
 // exp is the hardware's 2^x (1 ulp) of x log2(e); the product's rounding makes
@@ -189,5 +215,31 @@ __device__ __forceinline__ float half_bits_to_f32(uint32_t bits16) {
 __device__ __forceinline__ float mx4_scale(uint32_t byte) {
   return __builtin_bit_cast(float, byte ? byte << 23 : 0x00400000u);
 }
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// 8 neighbouring values, as they lie in memory.
+template <int ET>
+struct Eight {
+  u32x4 raw[ET == BMM_ELEM_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* src, int64_t at) {
+    const int64_t size = ET == BMM_ELEM_F32 ? 4 : 2;
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(src) + at * size);
+    raw[0] = p[0];
+    if constexpr (ET == BMM_ELEM_F32) raw[1] = p[1];
+  }
+  __device__ __forceinline__ void zero() {
+    raw[0] = u32x4{0, 0, 0, 0};
+    if constexpr (ET == BMM_ELEM_F32) raw[1] = raw[0];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (ET == BMM_ELEM_F32) {
+      const uint32_t bits = raw[i >> 2][i & 3];   // (a cast of the element itself takes element 0)
+      return __builtin_bit_cast(float, bits);
+    } else
+      return half_bits_to_f32<ET == BMM_ELEM_BF16 ? kBF16 : kF16>((raw[0][i >> 1] >> (16 * (i & 1))) &
+                                                                  0xffffu);
+  }
+};
 
 }  // namespace bmm

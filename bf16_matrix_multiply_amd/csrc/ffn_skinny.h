@@ -30,7 +30,24 @@ __device__ __forceinline__ u32x4 load_at(__amdgpu_buffer_rsrc_t rsrc, uint32_t o
              : __builtin_amdgcn_raw_buffer_load_b128(rsrc, off, 0, 0);
 }
 
-template <int DT, int EPI, int MR, int NB, int W>
+// 16 x 16 x 64 8-bit integers; the sums are whole numbers held in acc's bits.
+__device__ __forceinline__ f32x4 mfma_i8(u32x4 b, u32x4 a, f32x4 acc) {
+  return __builtin_bit_cast(
+      f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b),
+                                                   __builtin_bit_cast(i32x4, a),
+                                                   __builtin_bit_cast(i32x4, acc), 0, 0, 0));
+}
+
+// Sums of two waves.
+template <int DT>
+__device__ __forceinline__ f32x4 add(f32x4 x, f32x4 y) {
+  if constexpr (DT == kI8)
+    return __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, x) + __builtin_bit_cast(i32x4, y));
+  else
+    return x + y;
+}
+
+template <int DT, int EPI, int GRP, int MR, int NB, int W>
 __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
   constexpr bool k4 = DT == kMX4;
   constexpr int kSteps = 4;                           // steps whose loads are sent together
@@ -62,8 +79,24 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int64_t batch = blockIdx.z;
-  const int64_t m0 = int64_t(blockIdx.y) * (16 * MR);
+  int64_t batch = blockIdx.z;
+  int64_t m0 = int64_t(blockIdx.y) * (16 * MR);
+  int64_t d_row = batch * p.M, a_off = batch * p.a_bs;   // first row of D; elements
+  bool empty = false;
+  if constexpr (GRP == kGroupRows) {
+    Groups groups;
+    groups.init(p.ends, int(p.batch), int(p.M), lane);
+    const auto tiles = groups.tiles<16 * MR>(p.zero_tail);
+    if (int(blockIdx.y) >= tiles.total) return;
+    const Group at = groups.find<16 * MR>(tiles, int(blockIdx.y));
+    empty = at.e == int(p.batch);   // the rows behind the last group: an empty sum
+    batch = empty ? 0 : at.e;
+    m0 = at.tile * (16 * MR);
+    d_row = at.start;
+    a_off = at.start * p.lda;
+    p.M = at.rows;
+    if (empty) p.K = 0;
+  }
   const int64_t n0 = int64_t(blockIdx.x) * (EPI == kGated ? 8 : 16) * NB;
   auto column = [&](int j) { return n0 + 16 * (EPI == kGated ? j >> 1 : j); };
 
@@ -76,7 +109,7 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
                                    n0 / 16 * row16_b
                              : bases_b[0];
   const char* const base_a =
-      static_cast<const char*>(p.a) + (k4 ? 1 : 2) * batch * p.a_bs + m0 / 16 * row16_a;
+      static_cast<const char*>(p.a) + (k4 ? 1 : 2) * a_off + m0 / 16 * row16_a;
   uint32_t ob[4], oa[4];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
@@ -144,6 +177,8 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
         for (int j = 0; j < NB; ++j)
           if constexpr (k4)
             acc[i][j] = mfma_mx4<u>(fb[u][j], fa[u][i], xb[j], xa[i], acc[i][j]);
+          else if constexpr (DT == kI8)
+            acc[i][j] = mfma_i8(fb[u][j], fa[u][i], acc[i][j]);
           else
             acc[i][j] = mfma_16x16x32<DT>(fb[u][j], fa[u][i], acc[i][j]);
     });
@@ -162,14 +197,14 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
 #pragma unroll
     for (int i = 0; i < MR; ++i)
 #pragma unroll
-      for (int j = 0; j < NB; ++j) acc[i][j] += red[wave][i][j][lane];
+      for (int j = 0; j < NB; ++j) acc[i][j] = add<DT>(acc[i][j], red[wave][i][j][lane]);
     put(wave);
   }
   __syncthreads();
   auto total = [&](int i, int j, int l) {
     f32x4 v = red[0][i][j][l];
 #pragma unroll
-    for (int w = 1; w < W / 2; ++w) v += red[w][i][j][l];
+    for (int w = 1; w < W / 2; ++w) v = add<DT>(v, red[w][i][j][l]);
     return v;
   };
   auto store = [&](void* d, int64_t at, f32x4 v) {
@@ -187,9 +222,21 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
     const int l = o % kWave, j = o / kWave % kOuts, i = o / kWave / kOuts;
     const int64_t m = m0 + 16 * i + (l & 15), n = n0 + 16 * j + 4 * (l >> 4);
     if (m >= p.M || n >= p.N) continue;
-    const int64_t at = (batch * p.M + m) * p.ldd + n;
+    const int64_t at = (d_row + m) * p.ldd + n;
+    // 8-bit integers: the sums times the scales of their row and columns
+    auto scaled = [&](f32x4 v, const float* sb) {
+      if constexpr (DT == kI8) {
+        if (empty) return v;   // zeros, whatever the tail's scales hold
+        const float x = p.sa[d_row + m];
+        const f32x4 y = load16f(sb + batch * p.N + n);
+        const i32x4 q = __builtin_bit_cast(i32x4, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = float(q[e]) * x * y[e];
+      }
+      return v;
+    };
     if constexpr (EPI == kGated) {
-      const f32x4 gv = total(i, 2 * j, l), uv = total(i, 2 * j + 1, l);
+      const f32x4 gv = scaled(total(i, 2 * j, l), p.sb0), uv = scaled(total(i, 2 * j + 1, l), p.sb1);
       f32x4 h;
       switch (p.act) {
         case BMM_ACT_SILU: h = gate<BMM_ACT_SILU>(gv, uv); break;
@@ -203,18 +250,21 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
         store(p.d2, at, uv);
       }
     } else {
-      store(p.d, at, total(i, j, l));
+      store(p.d, at, scaled(total(i, j, l), p.sb0));
     }
   }
 }
 
-template <int DT, int EPI, int MR, int NB, int W>
+template <int DT, int EPI, int GRP, int MR, int NB, int W>
 hipError_t launch_skinny_of(const TileArgs& p, hipStream_t s) {
   const int64_t cols = (EPI == kGated ? 8 : 16) * NB;
-  const int64_t x = (p.N + cols - 1) / cols, y = (p.M + 16 * MR - 1) / (16 * MR);
-  if (x > 0x7fffffff || y > 65535 || p.batch > 65535) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((ffn_skinny_kernel<DT, EPI, MR, NB, W>),
-                     dim3(unsigned(x), unsigned(y), unsigned(p.batch)), dim3(W * kWave), 0, s, p);
+  const int64_t x = (p.N + cols - 1) / cols;
+  const int64_t y = GRP == kGroupRows ? most_row_tiles(p.M, p.batch, 16 * MR)
+                                      : (p.M + 16 * MR - 1) / (16 * MR);
+  const int64_t z = GRP == kGroupRows ? 1 : p.batch;
+  if (x > 0x7fffffff || y > 65535 || z > 65535) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((ffn_skinny_kernel<DT, EPI, GRP, MR, NB, W>),
+                     dim3(unsigned(x), unsigned(y), unsigned(z)), dim3(W * kWave), 0, s, p);
   return hipGetLastError();
 }
 
@@ -237,9 +287,19 @@ hipError_t launch_skinny_of(const TileArgs& p, hipStream_t s) {
 template <int DT, int EPI>
 hipError_t launch_skinny(const TileArgs& p, hipStream_t s) {
   constexpr int kWide = DT == kMX4 ? 4 : 2;
-  if (p.M <= 16) return launch_skinny_of<DT, EPI, 1, 2, 8>(p, s);
-  if (p.M <= 32) return launch_skinny_of<DT, EPI, 2, kWide, 8>(p, s);
-  return launch_skinny_of<DT, EPI, 4, kWide, 8>(p, s);
+  if (p.M <= 16) return launch_skinny_of<DT, EPI, kWhole, 1, 2, 8>(p, s);
+  if (p.M <= 32) return launch_skinny_of<DT, EPI, kWhole, 2, kWide, 8>(p, s);
+  return launch_skinny_of<DT, EPI, kWhole, 4, kWide, 8>(p, s);
+}
+
+// By groups: blocks of 16 rows, or of 32 or 64 where the groups that have rows have
+// more in the mean (the host does not know the groups, only T and E).
+template <int DT, int EPI>
+hipError_t launch_skinny_groups(const TileArgs& p, hipStream_t s) {
+  const int64_t groups = p.batch < p.M ? p.batch : p.M, mean = groups > 0 ? p.M / groups : 0;
+  if (mean <= 8) return launch_skinny_of<DT, EPI, kGroupRows, 1, 2, 8>(p, s);
+  if (mean <= 24) return launch_skinny_of<DT, EPI, kGroupRows, 2, 2, 8>(p, s);
+  return launch_skinny_of<DT, EPI, kGroupRows, 4, 2, 8>(p, s);
 }
 
 }  // namespace ffn

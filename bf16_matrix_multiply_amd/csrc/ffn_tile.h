@@ -7,6 +7,11 @@
 //   dW = [dG | dU]^T X               A transposed, B transposed            store
 //   D  = A B^T, 4-bit                A, B 4-bit                            store
 //   H  = act(..) * (..), 4-bit       A, B 4-bit, two sources               gated
+//   Y  = X W^T                       A rows,       B packed                store
+// The first, the last and the two sums of the second and third also by groups
+// (ffn_groups.h): tiles of a group's rows with the group's own B, or for dW sums
+// over a group's rows. The first and the last also with 8-bit integers, two of
+// which take the place of a 16-bit value everywhere but in the MFMA (16x16x64).
 //
 // "rows": row-major, the summed axis contiguous. "transposed": row-major with
 // the summed axis across rows (the matrix enters as its transpose). "packed":
@@ -66,12 +71,15 @@
 #include <type_traits>
 
 #include "ffn.h"
+#include "ffn_groups.h"
 
 namespace bmm {
 namespace ffn {
 
-enum Src : int { kRows, kTrans, kPacked2, kPackedT2, kCodes, kCodes2 };
+enum Src : int { kRows, kTrans, kPacked, kPacked2, kPackedT2, kCodes, kCodes2 };
 enum Epi : int { kStore, kGated };
+// By groups: of the rows of A and D, or of the summed rows of A and B.
+enum Grouped : int { kWhole, kGroupRows, kGroupSums };
 
 constexpr uint32_t kXcds = 8;
 // M tiles in a band: an XCD works on 4 x 8 tiles at a time, whose 12 panels share
@@ -82,6 +90,7 @@ constexpr int kBufferFlags = 0x00020000;           // raw, untyped buffer
 constexpr uint32_t kOutOfRange = 0x7fffffffu;      // an offset past every buffer's end
 
 typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
@@ -210,13 +219,15 @@ struct Loader {
       for (int r = 0; r < T / 64; ++r)
         off[r] = r0 + 64 * r + 16 * (lane >> 4) < n ? uint32_t(wave * n * 16 + 1024 * r + 16 * x)
                                                     : kOutOfRange;
-    } else if constexpr (SRC == kPacked2) {
+    } else if constexpr (SRC == kPacked || SRC == kPacked2) {
       k_lane = (lane & 16) + 8 * (lane & 1);
       step = 512;
-      base0 = static_cast<const char*>(wave & 1 ? s1 : s0) + 2 * (batch_off + r0 * p.K);
+      base0 = static_cast<const char*>(SRC == kPacked2 && (wave & 1) ? s1 : s0) +
+              2 * (batch_off + r0 * p.K);
 #pragma unroll
       for (int r = 0; r < T / 64; ++r) {
-        const int half = 2 * (2 * r + (wave >> 1)) + (lane >> 5);   // 8-column atom row
+        const int piece = SRC == kPacked2 ? 2 * r + (wave >> 1) : 4 * r + wave;
+        const int half = 2 * piece + (lane >> 5);   // 8-column atom row
         off[r] = r0 + 8 * half < n ? uint32_t(half * p.K * 16 + 16 * (lane & 31)) : kOutOfRange;
       }
     } else {
@@ -289,7 +300,7 @@ struct Reader {
         // its stage, and waits for every load in flight where it cannot
         asm volatile("" : "+v"(at4[b]));
       }
-    } else if constexpr (SRC == kPacked2) {
+    } else if constexpr (SRC == kPacked || SRC == kPacked2) {
       at[0] = 1024 * first + 512 * (i >> 3) + 256 * (g >> 1) + 32 * (i & 7) + 16 * (g & 1);
     } else {
       at[0] = 1024 * first + 16 * lane;
@@ -357,6 +368,8 @@ template <int DT>
 __device__ __forceinline__ void mfma(u32x4 b, u32x4 a, f32x4& acc) {
   if constexpr (DT == kBF16)
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+  else if constexpr (DT == kI8)   // (the accumulators hold whole numbers)
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
   else
     asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
@@ -421,7 +434,11 @@ constexpr int kNonTemporal = 2;
 // 256 rows: one workgroup a CU (a wave's 64 accumulators of 4 floats fill the
 // accumulator registers, so 128 x 128 of D come from 16 fragment reads);
 // 128 x 128: two workgroups a CU.
-template <int DT, int SRCA, int SRCB, int EPI, int TM, int TN>
+//
+// By groups a workgroup finds its tile's group first (about 1 us); workgroups past
+// the last tile, whose number the host only knows a bound of, end there. Rows
+// behind the last group are a group whose sum is empty: its tiles store zeros.
+template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
 __global__ __launch_bounds__(kTileWaves* kWave)
 __attribute__((amdgpu_waves_per_eu(TM == 256 ? 1 : 2, TM == 256 ? 1 : 2)))
 void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
@@ -439,27 +456,58 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
+  Groups groups;
+  Groups::Tiles<TM> row_tiles;
+  if constexpr (GRP != kWhole)
+    groups.init(p.ends, int(p.batch), int(GRP == kGroupRows ? p.M : p.K), lane);
+  if constexpr (GRP == kGroupRows) {
+    row_tiles = groups.tiles<TM>(p.zero_tail);
+    MT = row_tiles.total;
+    n_tiles = MT * NT;
+  }
   const uint32_t splits = p.splits > 1 ? p.splits : 1, total = n_tiles * splits;
+  if (GRP == kGroupRows && blockIdx.x >= total) return;
   constexpr int kValues = slab_values(SRCA);
-  const int64_t slabs = (p.K + kValues - 1) / kValues;
 
   Loader<SRCA, TM> la;
   Loader<SRCB, TN> lb;
   Scales ca, cb0, cb1;
   uint32_t work = xcd_run(blockIdx.x, total), split = 0;
-  int64_t s0 = 0, s1 = slabs;   // the slabs to sum
   if (splits > 1) {
     split = work / n_tiles;
     work -= split * n_tiles;
+  }
+  TileAt t = tile_at(work, MT, NT, GRP != kGroupRows && p.batch > 1);
+  int64_t a_off = t.b * p.a_bs, b_off = t.b * p.b_bs;   // elements (4-bit codes: bytes)
+  int64_t d_row = 0;                                    // first row of D of the group
+  bool empty = false;                                   // the tail
+  if constexpr (GRP == kGroupRows) {
+    const Group at = groups.find<TM>(row_tiles, int(t.mt));
+    empty = at.e == int(p.batch);
+    t.b = empty ? 0 : at.e;
+    t.mt = at.tile;
+    a_off = at.start * p.lda;
+    b_off = t.b * p.b_bs;
+    d_row = at.start;
+    p.M = at.rows;
+    if (empty) p.K = p.b_sum = p.b_rows = 0;
+  } else if constexpr (GRP == kGroupSums) {
+    const Group at = groups.at(int(t.b));
+    a_off = at.start * p.lda;
+    b_off = at.start * p.ldb;
+    p.K = at.rows;
+  }
+  const int64_t slabs = (p.K + kValues - 1) / kValues;
+  int64_t s0 = 0, s1 = slabs;   // the slabs to sum
+  if (splits > 1) {
     // (a split starts at an even slab: rows come two slabs at a time)
     const uint32_t pairs = uint32_t((slabs + 1) / 2), q = pairs / splits, r = pairs % splits;
     s0 = 2 * (int64_t(split) * q + (split < r ? split : r));
     if (split + 1 < splits) s1 = s0 + 2 * (q + (split < r ? 1 : 0));
   }
-  const TileAt t = tile_at(work, MT, NT, p.batch > 1);
   const int64_t m0 = t.mt * TM, n0 = t.nt * kCols;
-  la.init(p, p.a, nullptr, t.b * p.a_bs, p.lda, m0, p.M, s1, lane, wave);
-  lb.init(p, p.b0, p.b1, t.b * p.b_bs, p.ldb, n0, p.N, s1, lane, wave);
+  la.init(p, p.a, nullptr, a_off, p.lda, m0, p.M, s1, lane, wave);
+  lb.init(p, p.b0, p.b1, b_off, p.ldb, n0, p.N, s1, lane, wave);
   if constexpr (DT == kMX4) {
     ca.init(p.as, t.b * p.as_bs, p.K, m0, p.M);
     cb0.init(p.bs0, t.b * p.bs_bs, p.K, n0, p.N);
@@ -608,9 +656,45 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
 #pragma unroll
     for (int j = 0; j < kBN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read from here on only
   const int64_t row = m0 + 16 * kBM * wm, col = n0 + (EPI == kGated ? 8 : 16) * kBN * wn;
+  // 8-bit integers: the scales of this lane's rows, and of its columns of each block
+  float scale_a[8];
+  f32x4 scale_b[8];
+  if constexpr (DT == kI8) {
+    const int64_t left = empty || p.M < row ? 0 : p.M - row, cols = empty || p.N < col ? 0 : p.N - col;
+    const auto sa = buffer(p.sa + (GRP == kGroupRows ? d_row : t.b * p.M) + row,
+                           uint32_t(left < 16 * kBM ? left : 16 * kBM) * 4);
+    const uint32_t bytes = uint32_t(cols < 16 * kBN ? cols : 16 * kBN) * 4;
+    const auto sb0 = buffer(p.sb0 + t.b * p.N + col, bytes);
+    const auto sb1 = buffer((EPI == kGated ? p.sb1 : p.sb0) + t.b * p.N + col, bytes);
+#pragma unroll
+    for (int i = 0; i < kBM; ++i)
+      scale_a[i] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(sa, 64 * i + 4 * (lane & 15), 0, 0));
+#pragma unroll
+    for (int j = 0; j < kBN; ++j) {
+      const int at = EPI == kGated ? 64 * (j >> 1) + 16 * g : 64 * j + 16 * g;
+      scale_b[j] = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(EPI == kGated && (j & 1) ? sb1 : sb0, at, 0, 0));
+    }
+  }
+  // The sums of block (i, j); 8-bit integers: those values times the scales.
+  auto sums = [&](int i, int j) {
+    if constexpr (DT == kI8) {
+      const f32x4 v = sum(acc[i][j]);
+      f32x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = v[e];   // (a cast of the element itself takes element 0)
+        r[e] = float(__builtin_bit_cast(int, x)) * scale_a[i] * scale_b[j][e];
+      }
+      return r;
+    } else {
+      return acc[i][j];
+    }
+  };
   constexpr int kPairsN = EPI == kGated ? kBN / 4 : kBN / 2;   // 32-column pieces
   // float32 results: partial sums, and the 4-bit product's where it is asked for
-  const bool wide = EPI == kStore && (DT == kMX4 ? p.out_type == BMM_ELEM_F32 : splits > 1);
+  const bool wide = EPI == kStore && (any_output(DT) ? p.out_type == BMM_ELEM_F32 : splits > 1);
   // (192 columns: 48 of H a wave, the last 16 by themselves)
   constexpr bool kLast = EPI == kGated && kBN % 4 != 0;
   u32x4 out[8][2];
@@ -622,15 +706,15 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
-          out[i][j] = join16<T>(gate<A>(acc[i][4 * j], acc[i][4 * j + 1]),
-                                gate<A>(acc[i][4 * j + 2], acc[i][4 * j + 3]));
+          out[i][j] = join16<T>(gate<A>(sums(i, 4 * j), sums(i, 4 * j + 1)),
+                                gate<A>(sums(i, 4 * j + 2), sums(i, 4 * j + 3)));
       if constexpr (kLast) {
 #pragma unroll
-        for (int i = 0; i < kBM; ++i) last[i] = pack4<T>(gate<A>(acc[i][kBN - 2], acc[i][kBN - 1]));
+        for (int i = 0; i < kBM; ++i) last[i] = pack4<T>(gate<A>(sums(i, kBN - 2), sums(i, kBN - 1)));
       }
     };
     auto gate_type = [&](auto a) {
-      if constexpr (DT != kMX4) gate_all(std::integral_constant<int, DT>{}, a);
+      if constexpr (!any_output(DT)) gate_all(std::integral_constant<int, DT>{}, a);
       else if (p.out_type == BMM_ELEM_BF16) gate_all(std::integral_constant<int, kBF16>{}, a);
       else gate_all(std::integral_constant<int, kF16>{}, a);
     };
@@ -656,7 +740,8 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   };
   if constexpr (EPI == kGated) {
     auto store = [&](void* d, auto value, auto last_value) {
-      const auto to = out_rows(static_cast<uint16_t*>(d) + (t.b * p.M + row) * ld + col,
+      const auto to = out_rows(static_cast<uint16_t*>(d) +
+                                   ((GRP == kGroupRows ? d_row : t.b * p.M) + row) * ld + col,
                                row_bytes, p.M - row, 16 * kBM);
       offsets();
 #pragma unroll
@@ -673,7 +758,7 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
       }
     };
     store(p.d, [&](int i, int j) { return out[i][j]; }, [&](int i) { return last[i]; });
-    if constexpr (DT != kMX4) {
+    if constexpr (!any_output(DT)) {
       if (p.d1) {
         store(p.d1, [&](int i, int j) { return join16<DT>(acc[i][4 * j], acc[i][4 * j + 2]); },
               [&](int i) { return pack4<DT>(acc[i][kBN - 2]); });
@@ -687,9 +772,9 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     const bool parts = splits > 1;
     const char* d = parts ? reinterpret_cast<char*>(p.part + split * p.part_floats)
                           : static_cast<char*>(p.d);
-    const int64_t rows = parts ? p.M : p.rows0;
-    const auto to = out_rows(d + ((t.b * rows + row) * ld + col) * size, row_bytes,
-                             rows - row, 16 * kBM);
+    const int64_t rows = GRP == kGroupRows || parts ? p.M : p.rows0;
+    const auto to = out_rows(d + (((GRP == kGroupRows ? d_row : t.b * rows) + row) * ld + col) * size,
+                             row_bytes, rows - row, 16 * kBM);
     auto to1 = to;
     int second = kBM;   // first block of 16 rows that goes to d1
     if constexpr (SRCA == kTrans) {
@@ -707,8 +792,9 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     };
     float rescale = 1.f;
     if constexpr (DT == kF16) rescale = p.rescale ? *p.rescale : 1.f;
-    auto result = [&](f32x4 acc) {
-      const f32x4 v = sum(acc);
+    auto result = [&](int i, int j) {
+      if constexpr (DT == kI8) return sums(i, j);
+      const f32x4 v = sum(acc[i][j]);
       return DT == kF16 ? v * rescale : v;
     };
     auto store16 = [&](auto type) {
@@ -716,16 +802,16 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
-          store(i, j, join16<decltype(type)::value>(result(acc[i][2 * j]), result(acc[i][2 * j + 1])),
+          store(i, j, join16<decltype(type)::value>(result(i, 2 * j), result(i, 2 * j + 1)),
                 std::integral_constant<int, kNonTemporal>{});
     };
     auto store32 = [&](auto nt) {
 #pragma unroll
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
-        for (int j = 0; j < kBN; ++j) store(i, j, __builtin_bit_cast(u32x4, acc[i][j]), nt);
+        for (int j = 0; j < kBN; ++j) store(i, j, __builtin_bit_cast(u32x4, sums(i, j)), nt);
     };
-    if constexpr (DT != kMX4) {
+    if constexpr (!any_output(DT)) {
       if (wide) store32(std::integral_constant<int, 0>{});
       else store16(std::integral_constant<int, DT>{});
     } else {
@@ -736,28 +822,29 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   }
 }
 
-template <int DT, int SRCA, int SRCB, int EPI, int TM, int TN>
+template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
 hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
   const int64_t cols = EPI == kGated ? TN / 2 : TN;
-  const int64_t MT = (p.M + TM - 1) / TM, NT = (p.N + cols - 1) / cols;
-  const int64_t n = p.batch * MT * NT;
+  const int64_t MT = GRP == kGroupRows ? most_row_tiles(p.M, p.batch, TM) : (p.M + TM - 1) / TM;
+  const int64_t NT = (p.N + cols - 1) / cols;
+  const int64_t n = (GRP == kGroupRows ? 1 : p.batch) * MT * NT;
   const int64_t splits = p.splits > 1 ? p.splits : 1;
   if (n == 0) return hipSuccess;
   if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37)
     return hipErrorInvalidConfiguration;
-  auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, TM, TN>;
+  auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, GRP, TM, TN>;
   hipLaunchKernelGGL(kern, dim3(unsigned(n * splits)), dim3(kTileWaves * kWave), 0, s, p,
                      uint32_t(n), uint32_t(MT), uint32_t(NT));
   return hipGetLastError();
 }
 
-template <int DT, int SRCA, int SRCB, int EPI>
+template <int DT, int SRCA, int SRCB, int EPI, int GRP = kWhole>
 hipError_t launch_tile(const TileArgs& p, hipStream_t s) {
   switch (p.tile) {
-    case kTile256: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 256>(p, s);
-    case kTile256x128: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 128>(p, s);
-    case kTile256x192: return launch_tile_of<DT, SRCA, SRCB, EPI, 256, 192>(p, s);
-    default: return launch_tile_of<DT, SRCA, SRCB, EPI, 128, 128>(p, s);
+    case kTile256: return launch_tile_of<DT, SRCA, SRCB, EPI, GRP, 256, 256>(p, s);
+    case kTile256x128: return launch_tile_of<DT, SRCA, SRCB, EPI, GRP, 256, 128>(p, s);
+    case kTile256x192: return launch_tile_of<DT, SRCA, SRCB, EPI, GRP, 256, 192>(p, s);
+    default: return launch_tile_of<DT, SRCA, SRCB, EPI, GRP, 128, 128>(p, s);
   }
 }
 

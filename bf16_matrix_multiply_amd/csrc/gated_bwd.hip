@@ -15,7 +15,7 @@
 // largest then keep all their digits, and what vanishes is below 2^-39 of it. No
 // operand is transposed or repacked in memory: the products read X, [dG | dU]
 // and the packed weights through the transposing LDS reads.
-#include "ffn_tile.h"
+#include "ffn_split.h"
 
 namespace bmm {
 namespace {
@@ -44,8 +44,6 @@ __device__ __forceinline__ void slopes_of_eight(const uint16_t* dh, const uint16
     }
 }
 
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
 // The largest of the workgroup's values, in every thread.
 __device__ __forceinline__ uint32_t block_max(uint32_t x) {
   __shared__ uint32_t of_wave[kThreads / kWave];
@@ -59,6 +57,14 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
   return x;
 }
 
+// n items, per_row a row, held to the rows before *end (groups: what lies behind the
+// last one is not read).
+__device__ __forceinline__ int64_t rows_until(const int32_t* end, int64_t n, int64_t per_row) {
+  if (!end) return n;
+  const int64_t rows = *end, m = rows > 0 ? rows * per_row : 0;
+  return m < n ? m : n;
+}
+
 // The largest finite magnitude of dG and dU that each workgroup meets, as float32
 // bits (which are ordered like the values). Bound by memory: 8192 x 8192 72-79 us = 5.1-5.6
 // TB/s; of the whole backward pass 45 x 528 -> 1368 3 of 26 us, 32773 x 512 -> 1024
@@ -68,9 +74,11 @@ __global__ __launch_bounds__(kThreads) void peaks_kernel(uint32_t* __restrict__ 
                                                          const uint16_t* __restrict__ dh,
                                                          const uint16_t* __restrict__ g,
                                                          const uint16_t* __restrict__ u, int64_t n,
-                                                         int64_t F, int64_t ld) {
+                                                         int64_t F, int64_t ld,
+                                                         const int32_t* __restrict__ end) {
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t per_row = F / 8;
+  n = rows_until(end, n, per_row);
   uint32_t top = 0;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
     const int64_t row = i / per_row, f = 8 * (i % per_row);
@@ -95,11 +103,13 @@ __global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__
                                                           const uint16_t* __restrict__ u,
                                                           int64_t n, int64_t F, int64_t Fp,
                                                           int64_t ld,
+                                                          const int32_t* __restrict__ end,
                                                           const uint32_t* __restrict__ peaks,
                                                           int n_peaks,
                                                           float* __restrict__ rescale) {
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t per_row = Fp / 8;
+  n = rows_until(end, n, per_row);
   float scale = 1.f;
   if constexpr (DT == kF16) {
     uint32_t top = 0;
@@ -133,53 +143,9 @@ __global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__
   }
 }
 
-// The partial sums of a split product, added in order and rounded once (f16: after
-// the factor at p.rescale). Rows
-// as in TileArgs: r < rows0 to d, row1 <= r < row1 + rows0 to d1.
-template <int DT>
-__global__ __launch_bounds__(kThreads) void join_kernel(TileArgs p, int64_t n8) {
-  const int64_t stride = int64_t(gridDim.x) * kThreads;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n8; i += stride) {
-    const int64_t row = 8 * i / p.N, col = 8 * i % p.N;
-    const int64_t b = row / p.M, m = row % p.M;
-    const bool second = m >= p.row1;
-    const int64_t r = second ? m - p.row1 : m;
-    if (r >= p.rows0) continue;
-    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-    for (int s = 0; s < p.splits; ++s) {
-      const float* at = p.part + s * p.part_floats + 8 * i;
-      lo += load16f_nt(at);
-      hi += load16f_nt(at + 4);
-    }
-    if constexpr (DT == kF16) {
-      const float z = p.rescale ? *p.rescale : 1.f;
-      lo *= z;
-      hi *= z;
-    }
-    const u32x4 o = {pack2<DT>(lo[0], lo[1]), pack2<DT>(lo[2], lo[3]), pack2<DT>(hi[0], hi[1]),
-                     pack2<DT>(hi[2], hi[3])};
-    uint16_t* d = static_cast<uint16_t*>(second ? p.d1 : p.d);
-    *reinterpret_cast<u32x4*>(d + (b * p.rows0 + r) * p.ldd + col) = o;
-  }
-}
-
 unsigned grid_for(int64_t n) {
   const int64_t blocks = (n + kThreads - 1) / kThreads;
   return unsigned(blocks < 8192 ? blocks : 8192);
-}
-
-template <int DT>
-hipError_t join(const TileArgs& a, hipStream_t s) {
-  const int64_t n8 = a.batch * a.M * a.N / 8;
-  hipLaunchKernelGGL(join_kernel<DT>, dim3(grid_for(n8)), dim3(kThreads), 0, s, a, n8);
-  return hipGetLastError();
-}
-
-template <int DT, int SRCA, int SRCB>
-hipError_t product(const TileArgs& a, hipStream_t s) {
-  hipError_t e = ffn::launch_tile<DT, SRCA, SRCB, ffn::kStore>(a, s);
-  if (e == hipSuccess && a.splits > 1) e = join<DT>(a, s);
-  return e;
 }
 
 }  // namespace
@@ -191,7 +157,8 @@ int64_t gated_peaks(int64_t rows, int64_t F) {
 
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, uint32_t* peaks, float* rescale, hipStream_t s) {
+                               int act, const int32_t* end, uint32_t* peaks, float* rescale,
+                               hipStream_t s) {
   const int64_t Fp = (F + 31) / 32 * 32, n = rows * Fp / 8;
   if (n == 0) return hipSuccess;
   auto by_act = [&](auto fn) {
@@ -206,25 +173,35 @@ hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t
   if (dtype == kF16) {
     hipLaunchKernelGGL(by_act([](auto a) { return peaks_kernel<kF16, decltype(a)::value>; }),
                        dim3(unsigned(n_peaks)), dim3(kThreads), 0, s, peaks, dh, g, u, rows * F / 8,
-                       F, ld);
+                       F, ld, end);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   auto kern = dtype == kBF16 ? by_act([](auto a) { return slopes_kernel<kBF16, decltype(a)::value>; })
                              : by_act([](auto a) { return slopes_kernel<kF16, decltype(a)::value>; });
-  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld, peaks,
-                     n_peaks, rescale);
+  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld, end,
+                     peaks, n_peaks, rescale);
   return hipGetLastError();
 }
 
 hipError_t launch_gated_dx(const TileArgs& a, int dtype, hipStream_t s) {
-  return dtype == kBF16 ? product<kBF16, ffn::kRows, ffn::kPackedT2>(a, s)
-                        : product<kF16, ffn::kRows, ffn::kPackedT2>(a, s);
+  return dtype == kBF16 ? ffn::product<kBF16, ffn::kRows, ffn::kPackedT2>(a, s)
+                        : ffn::product<kF16, ffn::kRows, ffn::kPackedT2>(a, s);
 }
 
 hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
-  return dtype == kBF16 ? product<kBF16, ffn::kTrans, ffn::kTrans>(a, s)
-                        : product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
+  return dtype == kBF16 ? ffn::product<kBF16, ffn::kTrans, ffn::kTrans>(a, s)
+                        : ffn::product<kF16, ffn::kTrans, ffn::kTrans>(a, s);
+}
+
+hipError_t launch_grouped_dx(const TileArgs& a, int dtype, hipStream_t s) {
+  return dtype == kBF16 ? ffn::product<kBF16, ffn::kRows, ffn::kPackedT2, ffn::kGroupRows>(a, s)
+                        : ffn::product<kF16, ffn::kRows, ffn::kPackedT2, ffn::kGroupRows>(a, s);
+}
+
+hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s) {
+  return dtype == kBF16 ? ffn::product<kBF16, ffn::kTrans, ffn::kTrans, ffn::kGroupSums>(a, s)
+                        : ffn::product<kF16, ffn::kTrans, ffn::kTrans, ffn::kGroupSums>(a, s);
 }
 
 // The plan that a simple model finds fastest. A tile of each size takes so many
@@ -245,7 +222,11 @@ hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s) {
 // often the better ones (kept, 4096 x 256 -> 4096: 47 us, chosen 256 x 256 56; 16384 x
 // 256 -> 2048: 83, chosen 97; but 8192 x 256 -> 8192: 230, chosen 159), and 256 x 192
 // tiles, which write the last columns in pieces of 32 bytes, the slowest (369 there).
-TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
+namespace {
+
+// row_tiles(tm): tiles of tm rows; outputs: values that a split sum is held in.
+template <class Fn>
+TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool may_split) {
   struct Size {
     int64_t tm, tn, places;
     double slab, besides, first, later;
@@ -258,7 +239,7 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
   TilePlan best{kTile128, 1, 0};
   for (int size = 0; size < 4; ++size) {
     const Size& z = kSizes[size];
-    const double tiles = double(batch) * ((M + z.tm - 1) / z.tm) * ((N + z.tn - 1) / z.tn);
+    const double tiles = row_tiles(z.tm) * ((N + z.tn - 1) / z.tn);
     for (int splits : kSplits) {
       if (splits > 1 && (!may_split || slabs / splits < 8)) break;
       const double tile = double((slabs + splits - 1) / splits) * z.slab + z.besides;
@@ -266,11 +247,29 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
       const double a = rounds > 0 ? z.later : z.first;
       double cost = rounds * tile;
       if (fill > rounds) cost += tile * (a + (1 - a) * (fill - rounds));
-      if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * batch * double(M) * N;
+      if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * outputs;
       if ((size == 0 && splits == 1) || cost < best.ns) best = {size, splits, cost};
     }
   }
   return best;
+}
+
+}  // namespace
+
+TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
+  auto row_tiles = [&](int64_t tm) { return double(batch) * ((M + tm - 1) / tm); };
+  return plan_of(row_tiles, N, slabs, double(batch) * M * N, may_split);
+}
+
+// The host knows T rows and E groups, not how the rows fall on them: groups that have
+// rows have n in the mean, and the last tile of one is half full.
+TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool may_split) {
+  const double some = double(E < T ? E : T), n = some > 0 ? T / some : 0;
+  auto row_tiles = [&](int64_t tm) {
+    const double tiles = n / tm + (E > 1 ? 0.5 : 0);
+    return some * (tiles > 1 ? tiles : 1);
+  };
+  return plan_of(row_tiles, N, slabs, double(T) * N, may_split);
 }
 
 // Few rows: the weights are read once for up to 64 rows. Few-rows kernel / 128 x 128
@@ -288,6 +287,12 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
 int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs) {
   if (M <= 64 && batch <= 65535) return kSkinny;
   return plan_tiles(batch, M, N, slabs, false).tile;
+}
+
+int plan_group_forward(int64_t E, int64_t T, int64_t N, int64_t slabs) {
+  const int64_t some = E < T ? E : T;
+  if (some > 0 && T / some <= 48 && T / 16 + some < 65535) return kSkinny;
+  return plan_group_rows(E, T, N, slabs, false).tile;
 }
 
 }  // namespace bmm

@@ -34,32 +34,6 @@ struct Lane {
   }
 };
 
-// 8 neighbouring values, as they lie in memory.
-template <int ET>
-struct Eight {
-  u32x4 raw[ET == BMM_ELEM_F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* src, int64_t at) {
-    const int64_t size = ET == BMM_ELEM_F32 ? 4 : 2;
-    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const char*>(src) + at * size);
-    raw[0] = p[0];
-    if constexpr (ET == BMM_ELEM_F32) raw[1] = p[1];
-  }
-  __device__ __forceinline__ void zero() {
-    raw[0] = u32x4{0, 0, 0, 0};
-    if constexpr (ET == BMM_ELEM_F32) raw[1] = raw[0];
-  }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (ET == BMM_ELEM_F32) {
-      const uint32_t bits = raw[i >> 2][i & 3];   // (a cast of the element itself takes element 0)
-      return __builtin_bit_cast(float, bits);
-    } else
-      return half_bits_to_f32<ET == BMM_ELEM_BF16 ? kBF16 : kF16>((raw[0][i >> 1] >> (16 * (i & 1))) &
-                                                                  0xffffu);
-  }
-};
-
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-
 // The largest of four neighbouring lanes' values.
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   x = umax(x, uint32_t(__builtin_amdgcn_mov_dpp(int(x), 0xb1, 0xf, 0xf, true)));   // lanes 1 0 3 2

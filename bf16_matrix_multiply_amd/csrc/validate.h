@@ -70,6 +70,28 @@ Status check_mx4_product(const void* D, const uint8_t* A, const uint8_t* As, con
                          int64_t batch, int64_t M, int64_t N, int64_t K, int64_t ld, int32_t act,
                          int32_t elem_type);
 
+// Products by groups (validate_grouped.cpp). Extents alone; `what` prefixes the messages.
+Status check_grouped_desc(const bmm_grouped_desc* d, bool gated, const char* what);
+// Y = X W^T (W1, Y1 and Y2 null), or H, G and U from Wg and Wu.
+Status check_grouped(const uint16_t* Y, const uint16_t* Y1, const uint16_t* Y2, const uint16_t* X,
+                     const uint32_t* W, const uint32_t* W1, const int32_t* ends,
+                     const bmm_grouped_desc* d, bool gated);
+struct GroupedGrads {
+  const uint16_t *dX, *dW, *dW1;      // dW1: gated only
+  const uint16_t *dY, *G, *U, *X;     // gated: dY is dH
+  const uint32_t *W, *W1;
+};
+Status check_grouped_backward(const GroupedGrads& g, const int32_t* ends, const bmm_grouped_desc* d,
+                              bool gated, const void* workspace, int64_t workspace_bytes,
+                              int64_t need);
+Status check_i8_quantize(const void* src, const int8_t* codes, const float* scales, int64_t batch,
+                         int64_t rows, int64_t K, int64_t ld, int32_t elem_type);
+// Product (W1 null) or gated product.
+Status check_i8_product(const void* D, const int8_t* A, const float* sa, const uint32_t* W,
+                        const float* sw, const uint32_t* W1, const float* sw1, const int32_t* ends,
+                        const bmm_i8_desc* d, bool gated);
+Status check_group_plan(int32_t product, const bmm_grouped_desc& d);
+
 // Largest image (bytes) one box repeat may stage through LDS.
 constexpr int64_t kBoxImageLimit = 65536;
 

@@ -593,6 +593,192 @@ typedef enum {
 int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K,
                  int32_t* splits);
 
+/*
+ * ---- Products by groups of rows (the experts of a mixture) ----
+ *
+ * T rows lie sorted by group (by expert): group e of `groups` has the rows from
+ * ends[e - 1] up to ends[e], group 0 from 0, any number of them, also none. Rows
+ * from ends[groups - 1] on belong to no group (a batch padded to a fixed size):
+ * they are not read, and their outputs become zero with zero_tail and stay as
+ * they are without. ends is device memory and is read by the kernels only, so a
+ * captured graph takes other groups on every replay. Ends are held to 0 .. T and
+ * to be no smaller than the ones before: other values give meaningless outputs,
+ * but nothing outside of the matrices is touched.
+ *
+ * Extents of a product by groups.
+ *   groups     1 .. 4096
+ *   T          rows in all, below 2^31
+ *   N          width of the outputs (of the gated block), a multiple of 8, at
+ *              most 2^20
+ *   K          width of X, a multiple of 16, at most 2^21
+ *   ld_x       elements between rows of X: >= K, a multiple of 8, at most 2^21
+ *   ld_y       elements between rows of Y and dY (H, G, U and dH): >= N, a
+ *              multiple of 8, at most 2^21
+ *   dtype      bmm_dtype of every 16-bit value
+ *   act        bmm_act of the gated block (0 otherwise)
+ *   zero_tail  1: outputs of rows behind the last group become zero; 0: stay
+ */
+typedef struct {
+  int64_t groups;
+  int64_t T;
+  int64_t N;
+  int64_t K;
+  int64_t ld_x;
+  int64_t ld_y;
+  int32_t dtype;
+  int32_t act;
+  int32_t zero_tail;
+} bmm_grouped_desc;
+
+/*
+ * bmm_grouped_mma — Y = X W_e^T for the rows of each group e, in one kernel.
+ *
+ * Y    (T, ld_y), written in the first N columns of each row.
+ * X    (T, ld_x), the first K columns of each row are read.
+ * W    (groups, N/8, K/16, 8, 8) packed words (bmm_pack_operand, atom_rows 8).
+ * ends (groups) int32, as above.
+ * The sums are float32, rounded once. K = 0 gives zeros; T = 0 or N = 0 is a
+ * no-op.
+ * Errors: BMM_EINVAL, BMM_EALIGN, BMM_EOVERLAP (an output with an input or with
+ * another output; interleaved rows of one buffer are no overlap), BMM_EHIP.
+ */
+int bmm_grouped_mma(uint16_t* Y, const uint16_t* X, const uint32_t* W, const int32_t* ends,
+                    const bmm_grouped_desc* desc, void* stream);
+
+/*
+ * bmm_grouped_mma_backward — gradients of bmm_grouped_mma from dY.
+ *
+ *   dX = dY W_e for the rows of each group;  dW_e = dY^T X over group e's rows
+ *
+ * dX   (T, K) contiguous, or NULL when it is not wanted.
+ * dW   (groups, N, K) contiguous and row-major, or NULL. A group without rows
+ *      gets zeros.
+ * dY   (T, ld_y); X (T, ld_x); W may be NULL when dX is, X when dW is.
+ * Sums are float32, rounded once; the result is the same on every run.
+ * workspace  device memory of at least bmm_grouped_mma_backward_workspace_bytes
+ *            bytes, 16-byte aligned, overlapping nothing else; owned by the
+ *            caller, clobbered.
+ * Errors: as bmm_grouped_mma; BMM_EINVAL also for a missing or short workspace
+ * and when nothing is wanted.
+ */
+int bmm_grouped_mma_backward(uint16_t* dX, uint16_t* dW, const uint16_t* dY, const uint16_t* X,
+                             const uint32_t* W, const int32_t* ends, const bmm_grouped_desc* desc,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+int64_t bmm_grouped_mma_backward_workspace_bytes(const bmm_grouped_desc* desc);
+
+/*
+ * bmm_grouped_gated — H = act(X Wg_e^T) * (X Wu_e^T) for the rows of each group
+ * e, in one kernel: bmm_gated with weights of each group.
+ *
+ * H, G, U as Y of bmm_grouped_mma; G and U both or neither. Wg, Wu as its W.
+ */
+int bmm_grouped_gated(uint16_t* H, uint16_t* G, uint16_t* U, const uint16_t* X, const uint32_t* Wg,
+                      const uint32_t* Wu, const int32_t* ends, const bmm_grouped_desc* desc,
+                      void* stream);
+
+/*
+ * bmm_grouped_gated_backward — gradients of bmm_grouped_gated from dH and the
+ * kept projections: bmm_gated_backward with the weights and weight gradients of
+ * each group (dWg, dWu: (groups, N, K), zeros for a group without rows). For f16
+ * the largest magnitude that scales dG and dU is that of the call, of all groups.
+ */
+int bmm_grouped_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_t* dH,
+                               const uint16_t* G, const uint16_t* U, const uint16_t* X,
+                               const uint32_t* Wg, const uint32_t* Wu, const int32_t* ends,
+                               const bmm_grouped_desc* desc, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+int64_t bmm_grouped_gated_backward_workspace_bytes(const bmm_grouped_desc* desc);
+
+/*
+ * ---- 8-bit integers ----
+ *
+ * A row is K codes from -127 to 127 and a float32 scale; code times scale is the
+ * value. Activations are row-major codes. Weights are packed B operands of their
+ * codes, two neighbouring ones taken as a 16-bit value: bmm_pack_operand of the
+ * (rows, K/2) 16-bit matrix that the codes are, atom_rows 8, so (batch, N/8, K/32,
+ * 8, 8) words.
+ *
+ * bmm_i8_quantize — a row-major matrix to codes (batch, rows, K), contiguous, and
+ * scales (batch, rows).
+ *
+ * scale = max |x| / 127 over the row, in float32; code = 127 x / max |x|, the real
+ * quotient rounded to nearest, ties to even. A row of zeros gets scale 0 and codes
+ * 0; one with a NaN or an infinity scale NaN and codes 0.
+ * src  (batch, rows, ld_src) values of elem_type (BMM_ELEM_F32, _F16 or _BF16),
+ *      batch stride rows * ld_src, 16-byte aligned; ld_src >= K and a multiple of
+ *      8; K a multiple of 32, below 2^22. Zero batch or rows is a no-op; K = 0
+ *      writes zero scales.
+ * Errors: BMM_EINVAL, BMM_EALIGN, BMM_EOVERLAP, BMM_EHIP.
+ */
+int bmm_i8_quantize(int8_t* codes, float* scales, const void* src, int64_t batch, int64_t rows,
+                    int64_t K, int64_t ld_src, int32_t elem_type, void* stream);
+
+/*
+ * Extents of a product of 8-bit integers.
+ *   batch      independent products; with ends: the groups, 1 .. 4096
+ *   M          rows of A (with ends: in all, below 2^31)
+ *   N          columns of D, a multiple of 8, at most 2^20
+ *   K          codes of a row, a multiple of 32, below 2^17 (sums of 128 * 128 K
+ *              stay below 2^31)
+ *   ld_a       codes between rows of A: >= K, a multiple of 16, at most 2^22
+ *   ld_d       elements between rows of D: >= N, a multiple of 8, at most 2^21
+ *   elem_type  of D: BMM_ELEM_F32, _F16 or _BF16 (gated: _F16 or _BF16)
+ *   act        bmm_act of the gated block (0 otherwise)
+ *   zero_tail  with ends, as in bmm_grouped_desc
+ */
+typedef struct {
+  int64_t batch;
+  int64_t M;
+  int64_t N;
+  int64_t K;
+  int64_t ld_a;
+  int64_t ld_d;
+  int32_t elem_type;
+  int32_t act;
+  int32_t zero_tail;
+} bmm_i8_desc;
+
+/*
+ * bmm_i8_mma — D[m][n] = A_scales[m] B_scales[n] (sum over k of A[m][k] B[n][k]).
+ *
+ * D         (batch, M, ld_d), with ends (M, ld_d), of elem_type.
+ * A         (batch, M, ld_a) codes, batch stride M * ld_a; A_scales (batch, M).
+ * B         (batch, N/8, K/32, 8, 8) packed words; B_scales (batch, N).
+ * ends      NULL, or (batch) int32: the groups of A's rows, as bmm_grouped_mma;
+ *           A is then (M, ld_a) and A_scales (M).
+ * The sums are exact; they are rounded to float32, multiplied by the row's scale
+ * and then by the column's, and rounded to elem_type. K = 0 gives zeros (NaN where
+ * a scale is no finite number); zero batch (without ends), M or N is a no-op.
+ * Errors: BMM_EINVAL, BMM_EALIGN (16 bytes; A_scales 4), BMM_EOVERLAP, BMM_EHIP.
+ */
+int bmm_i8_mma(void* D, const int8_t* A, const float* A_scales, const uint32_t* B,
+               const float* B_scales, const int32_t* ends, const bmm_i8_desc* desc, void* stream);
+
+/* bmm_i8_gated — H = act(X Wg^T) * (X Wu^T) over 8-bit integers, the projections
+ * as bmm_i8_mma gives them in float32. */
+int bmm_i8_gated(void* H, const int8_t* X, const float* X_scales, const uint32_t* Wg,
+                 const float* Wg_scales, const uint32_t* Wu, const float* Wu_scales,
+                 const int32_t* ends, const bmm_i8_desc* desc, void* stream);
+
+/*
+ * bmm_group_plan — as bmm_ffn_plan, for the products by groups (T rows in all) and
+ * of 8-bit integers (groups 0: one weight, no groups). N is the width F of a gated
+ * block.
+ */
+typedef enum {
+  BMM_GROUPED_MMA = 0,
+  BMM_GROUPED_MMA_DX = 1,
+  BMM_GROUPED_MMA_DW = 2,
+  BMM_GROUPED_GATED = 3,
+  BMM_GROUPED_GATED_DX = 4,
+  BMM_GROUPED_GATED_DW = 5,
+  BMM_I8_MMA = 6,
+  BMM_I8_GATED = 7
+} bmm_group_product;
+
+int bmm_group_plan(int32_t product, int64_t groups, int64_t T, int64_t N, int64_t K,
+                   int32_t* splits);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char* bmm_last_error(void);
 
