@@ -103,6 +103,35 @@ struct Groups {
     return {e, __builtin_amdgcn_readlane(start, l), __builtin_amdgcn_readlane(rows, l), 0};
   }
 
+  // The slot-th group (up to 64 groups) when those of one and a half times the mean
+  // rows or more come first, then those of the mean or more, of half of it, and the
+  // others: work that takes as long as a group has rows is better begun with the
+  // largest, and the four classes cost a few instructions where a sort would cost as
+  // much as a tile of a small group.
+  __device__ __forceinline__ Group large_first(int slot) const {
+    if (per > 1) return at(slot);
+    int start = 0, rows = -1;
+    each([&](int, int s, int n) {
+      start = s;
+      rows = n;
+    });
+    const int mean = T / E, border[4] = {mean + mean / 2, mean, mean / 2, 0};
+    int rank = -1, before_class = 0;
+    bool free = rows >= 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const bool here = free && rows >= border[c];
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(here);
+      const int below = __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+      if (here) rank = before_class + below;
+      before_class += __builtin_popcountll(mask);
+      free = free && !here;
+    }
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == slot));
+    return {l, __builtin_amdgcn_readlane(start, l), __builtin_amdgcn_readlane(rows, l), 0};
+  }
+
   // Tiles of TM rows: those of group 0, of group 1, ...; with `tail`, then those of
   // the rows behind the last group, as group E.
   template <int TM>

@@ -136,6 +136,21 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t w, uint32_t n) {
   return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
+// Sums over groups of different length: an XCD that takes whole groups has too much
+// or too little to do, so each takes an eighth of every group's units (tiles, times
+// splits), side by side where there are enough of them.
+constexpr uint32_t kSpreadUnits = 64;
+__host__ __device__ __forceinline__ uint32_t spread_units(uint32_t units) {   // launched a group
+  return units < kSpreadUnits ? units : (units + kXcds - 1) / kXcds * kXcds;
+}
+// Workgroup -> (slot among the groups, unit of the group; past the end: none).
+__device__ __forceinline__ void spread(uint32_t w, uint32_t units, uint32_t& slot, uint32_t& unit) {
+  const uint32_t launched = spread_units(units);
+  slot = w / launched;
+  unit = w - slot * launched;
+  if (units >= kSpreadUnits) unit = unit % kXcds * (launched / kXcds) + unit / kXcds;
+}
+
 // Linear tile index -> (batch, M tile, N tile), in bands of kGroupM M tiles.
 __device__ __forceinline__ TileAt tile_at(uint32_t t, uint32_t MT, uint32_t NT, bool batched) {
   uint32_t b = 0;
@@ -472,12 +487,19 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   Loader<SRCA, TM> la;
   Loader<SRCB, TN> lb;
   Scales ca, cb0, cb1;
-  uint32_t work = xcd_run(blockIdx.x, total), split = 0;
+  uint32_t work, split = 0, slot = 0;
+  if constexpr (GRP == kGroupSums) {
+    n_tiles = MT * NT;   // of a group
+    spread(blockIdx.x, n_tiles * splits, slot, work);
+    if (work >= n_tiles * splits) return;
+  } else {
+    work = xcd_run(blockIdx.x, total);
+  }
   if (splits > 1) {
     split = work / n_tiles;
     work -= split * n_tiles;
   }
-  TileAt t = tile_at(work, MT, NT, GRP != kGroupRows && p.batch > 1);
+  TileAt t = tile_at(work, MT, NT, GRP == kWhole && p.batch > 1);
   int64_t a_off = t.b * p.a_bs, b_off = t.b * p.b_bs;   // elements (4-bit codes: bytes)
   int64_t d_row = 0;                                    // first row of D of the group
   bool empty = false;                                   // the tail
@@ -492,7 +514,8 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     p.M = at.rows;
     if (empty) p.K = p.b_sum = p.b_rows = 0;
   } else if constexpr (GRP == kGroupSums) {
-    const Group at = groups.at(int(t.b));
+    const Group at = groups.large_first(int(slot));
+    t.b = at.e;
     a_off = at.start * p.lda;
     b_off = at.start * p.ldb;
     p.K = at.rows;
@@ -833,8 +856,11 @@ hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
   if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37)
     return hipErrorInvalidConfiguration;
   auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, GRP, TM, TN>;
-  hipLaunchKernelGGL(kern, dim3(unsigned(n * splits)), dim3(kTileWaves * kWave), 0, s, p,
-                     uint32_t(n), uint32_t(MT), uint32_t(NT));
+  const int64_t grid = GRP == kGroupSums ? p.batch * spread_units(uint32_t(MT * NT * splits))
+                                         : n * splits;
+  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kTileWaves * kWave), 0, s, p, uint32_t(n),
+                     uint32_t(MT), uint32_t(NT));
   return hipGetLastError();
 }
 
