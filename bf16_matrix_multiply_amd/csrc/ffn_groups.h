@@ -40,22 +40,28 @@ __device__ __forceinline__ int lane_before(int x) {
   return __builtin_amdgcn_update_dpp(0, x, 0x138, 0xf, 0xf, false);   // wave_shr:1
 }
 
-// Tiles of TM rows that n rows take.
+// The tiles that n rows take: of TM rows, the last one perhaps not full; with tiles of
+// 256 rows a last one of at most 128 is a small one, of 128 rows.
 template <int TM>
-__device__ __forceinline__ int row_tiles(int n) {
-  return n / TM + (n % TM != 0);
+__device__ __forceinline__ int full_tiles(int n) {
+  return TM == 256 ? (n + 127) / 256 : (n + TM - 1) / TM;
+}
+template <int TM>
+__device__ __forceinline__ int small_tiles(int n) {
+  return TM == 256 && n % 256 > 0 && n % 256 <= 128;
 }
 
 // A group, the same in every lane: its index, its first row and its rows, and the
-// tile's index among the group's tiles.
+// first row of a tile within the group.
 struct Group {
-  int e, start, rows, tile;
+  int e, start, rows, at;
 };
 
 struct Groups {
   const int32_t* ends;
   int E, T, per;       // groups, rows, groups a lane
   int lane, before;    // where this lane's first group starts
+  int rank;            // this lane's group in the order of size (sort)
   int end0;            // and its end as read (kept: with 64 groups or fewer nothing is read again)
 
   __device__ __forceinline__ int end(int i, int from) const {   // this lane's i-th group
@@ -103,82 +109,100 @@ struct Groups {
     return {e, __builtin_amdgcn_readlane(start, l), __builtin_amdgcn_readlane(rows, l), 0};
   }
 
-  // The slot-th group (up to 64 groups) when those of one and a half times the mean
-  // rows or more come first, then those of the mean or more, of half of it, and the
-  // others: work that takes as long as a group has rows is better begun with the
-  // largest, and the four classes cost a few instructions where a sort would cost as
-  // much as a tile of a small group.
-  __device__ __forceinline__ Group large_first(int slot) const {
-    if (per > 1) return at(slot);
-    int start = 0, rows = -1;
-    each([&](int, int s, int n) {
-      start = s;
-      rows = n;
-    });
-    const int mean = T / E, border[4] = {mean + mean / 2, mean, mean / 2, 0};
-    int rank = -1, before_class = 0;
-    bool free = rows >= 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const bool here = free && rows >= border[c];
-      const uint64_t mask = __builtin_amdgcn_ballot_w64(here);
-      const int below = __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32),
-                                                  __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
-      if (here) rank = before_class + below;
-      before_class += __builtin_popcountll(mask);
-      free = free && !here;
+  // Orders the groups by size, the largest first (up to 64 groups; more stay in their
+  // order): rank is the place of this lane's group.
+  __device__ __forceinline__ void sort() {
+    rank = lane;
+    if (per > 1) return;
+    int rows = -1;
+    each([&](int, int, int n) { rows = n; });
+    int before_it = 0;
+    for (int j = 0; j < E; ++j) {
+      const int n = __builtin_amdgcn_readlane(rows, j);
+      before_it += n > rows || (n == rows && j < lane);
     }
-    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == slot));
-    return {l, __builtin_amdgcn_readlane(start, l), __builtin_amdgcn_readlane(rows, l), 0};
+    rank = lane < E ? before_it : kWave;
+  }
+  // The slot-th group in that order.
+  __device__ __forceinline__ Group sorted(int slot) const {
+    if (per > 1) return at(slot);
+    return at(__builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == slot)));
   }
 
-  // Tiles of TM rows: those of group 0, of group 1, ...; with `tail`, then those of
-  // the rows behind the last group, as group E.
+  // Tiles: those of group 0, of group 1, ...; with `tail`, then those of the rows behind
+  // the last group, as group E. Small ones are counted by themselves.
   template <int TM>
   struct Tiles {
     int first, own;        // tiles before this lane's groups, and theirs
+    int first_small, own_small;
     int grouped, total;    // tiles of all groups; with the tail's
+    int grouped_small, total_small;
     int end_all;           // the first row behind the last group
   };
   template <int TM>
   __device__ __forceinline__ Tiles<TM> tiles(bool tail) const {
     Tiles<TM> t;
-    int own = 0, last = before;
+    int last = before;
+    t.own = t.own_small = 0;
     each([&](int, int s, int n) {
-      own += row_tiles<TM>(n);
+      t.own += full_tiles<TM>(n);
+      t.own_small += small_tiles<TM>(n);
       last = s + n;
     });
-    const int sum = lanes_sum(own);
-    t.own = own;
-    t.first = sum - own;
-    t.grouped = __builtin_amdgcn_readlane(sum, kWave - 1);
     t.end_all = __builtin_amdgcn_readlane(last, kWave - 1);
-    t.total = t.grouped + (tail ? row_tiles<TM>(T - t.end_all) : 0);
+    const int behind = tail ? T - t.end_all : 0;
+    int sum = lanes_sum(t.own);
+    t.first = sum - t.own;
+    t.grouped = __builtin_amdgcn_readlane(sum, kWave - 1);
+    t.total = t.grouped + full_tiles<TM>(behind);
+    t.first_small = t.grouped_small = t.total_small = 0;
+    if constexpr (TM == 256) {
+      sum = lanes_sum(t.own_small);
+      t.first_small = sum - t.own_small;
+      t.grouped_small = __builtin_amdgcn_readlane(sum, kWave - 1);
+      t.total_small = t.grouped_small + small_tiles<TM>(behind);
+    }
     return t;
   }
   // The group of row tile r < total.
   template <int TM>
   __device__ __forceinline__ Group find(const Tiles<TM>& t, int r) const {
-    if (r >= t.grouped) return {E, t.end_all, T - t.end_all, r - t.grouped};
-    int e = 0, start = 0, rows = 0, tile = 0, left = r - t.first;
+    if (r >= t.grouped) return {E, t.end_all, T - t.end_all, (r - t.grouped) * TM};
+    return search(r, t.first, t.own, [](int n) { return full_tiles<TM>(n); }, TM);
+  }
+  // The group of small row tile r < total_small.
+  template <int TM>
+  __device__ __forceinline__ Group find_small(const Tiles<TM>& t, int r) const {
+    Group g = {E, t.end_all, T - t.end_all, 0};
+    if (r < t.grouped_small)
+      g = search(r, t.first_small, t.own_small, [](int n) { return small_tiles<TM>(n); }, 0);
+    g.at = g.rows / 256 * 256;
+    return g;
+  }
+
+ private:
+  // The group of item r, of which each group has items(rows) and this lane's `own` from
+  // `first` on; at: the item's number in the group times `step`.
+  template <class Fn>
+  __device__ __forceinline__ Group search(int r, int first, int own, Fn items, int step) const {
+    int e = 0, start = 0, rows = 0, item = 0, left = r - first;
     each([&](int i, int s, int n) {
-      const int k = row_tiles<TM>(n);
+      const int k = items(n);
       if (left >= 0 && left < k) {
         e = i;
         start = s;
         rows = n;
-        tile = left;
+        item = left;
       }
       left -= k;
     });
-    const uint64_t here = __builtin_amdgcn_ballot_w64(r >= t.first && r < t.first + t.own);
-    const int l = __builtin_ctzll(here);
+    const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(r >= first && r < first + own));
     return {__builtin_amdgcn_readlane(e, l), __builtin_amdgcn_readlane(start, l),
-            __builtin_amdgcn_readlane(rows, l), __builtin_amdgcn_readlane(tile, l)};
+            __builtin_amdgcn_readlane(rows, l), __builtin_amdgcn_readlane(item, l) * step};
   }
 };
 
-// The most tiles of TM rows that T rows in E groups and a tail can take.
+// The most tiles, small ones among them, that T rows in E groups and a tail can take.
 inline int64_t most_row_tiles(int64_t T, int64_t E, int64_t TM) {
   const int64_t some = E + 1 < T ? E + 1 : T;
   return (T + some * (TM - 1)) / TM;

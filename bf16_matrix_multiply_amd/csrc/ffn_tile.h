@@ -136,21 +136,6 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t w, uint32_t n) {
   return xcd * q + (xcd < r ? xcd : r) + k;
 }
 
-// Sums over groups of different length: an XCD that takes whole groups has too much
-// or too little to do, so each takes an eighth of every group's units (tiles, times
-// splits), side by side where there are enough of them.
-constexpr uint32_t kSpreadUnits = 64;
-__host__ __device__ __forceinline__ uint32_t spread_units(uint32_t units) {   // launched a group
-  return units < kSpreadUnits ? units : (units + kXcds - 1) / kXcds * kXcds;
-}
-// Workgroup -> (slot among the groups, unit of the group; past the end: none).
-__device__ __forceinline__ void spread(uint32_t w, uint32_t units, uint32_t& slot, uint32_t& unit) {
-  const uint32_t launched = spread_units(units);
-  slot = w / launched;
-  unit = w - slot * launched;
-  if (units >= kSpreadUnits) unit = unit % kXcds * (launched / kXcds) + unit / kXcds;
-}
-
 // Linear tile index -> (batch, M tile, N tile), in bands of kGroupM M tiles.
 __device__ __forceinline__ TileAt tile_at(uint32_t t, uint32_t MT, uint32_t NT, bool batched) {
   uint32_t b = 0;
@@ -322,6 +307,17 @@ struct Reader {
     }
   }
 
+  // Keeps the compiler from making the stages' addresses ahead, outside of a loop over
+  // tiles: it would not know what they point to any more, and wait as above.
+  __device__ __forceinline__ void renew() {
+    constexpr int n = SRC == kTrans || SRC == kPackedT2 ? 4 : SRC == kRows ? 2 : 1;
+#pragma unroll
+    for (int b = 0; b < n; ++b) {
+      asm volatile("" : "+v"(at[b]));
+      if constexpr (n == 4) asm volatile("" : "+v"(at4[b]));
+    }
+  }
+
   __device__ __forceinline__ u32x4 read(const char* stage, int f, int h) const {
     if constexpr (SRC == kTrans || SRC == kPackedT2) {
       const int block = 4096 * (f >> 2), b = f & 3;
@@ -443,98 +439,177 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(const void* d, int64_
 
 // Outputs are touched once: non-temporal, so that they do not push the operands
 // out of the caches (gated with projections kept, 8192 x 4096 -> 8192: 819
-// against 843 us). Partial sums stay: the join reads them right after.
+// against 843 us). Partial sums stay: the join reads them right after. By groups,
+// where the sums are short, the caches take the results faster: 24576 rows of 64
+// groups gated 2048 -> 1408, projections kept, 358 us against 370.
 constexpr int kNonTemporal = 2;
+
+// The kernel's arguments, read again: what a loop over tiles needs of them only
+// between two sums would otherwise be kept in (spilled) scalar registers.
+__device__ __forceinline__ const TileArgs& args_again() {
+  uint64_t at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(at));
+  return *(const TileArgs*)reinterpret_cast<const __attribute__((address_space(4))) TileArgs*>(at);
+}
+
+// Where a tile lies and what it sums. By groups rows, values and columns are below
+// 2^31.
+template <int GRP>
+struct Place {
+  using Int = std::conditional_t<GRP == kWhole, int64_t, int32_t>;
+  Int b;                 // batch or group
+  Int m0, n0;            // first row within the group, first column
+  Int M, K;              // rows of the group, values to sum
+  Int d_row;             // first row of D of the group
+  Int s0, s1;            // the slabs to sum
+  int64_t a_off, b_off;  // elements (4-bit codes: bytes) to the batch's or group's operands
+  uint32_t split;
+  bool empty;            // the rows behind the last group
+};
+
+// The slabs of split `at.split`.
+template <int GRP>
+__device__ __forceinline__ void slabs_of(Place<GRP>& at, int values, uint32_t splits) {
+  using Int = typename Place<GRP>::Int;
+  const Int slabs = (at.K + values - 1) / values;
+  at.s0 = 0;
+  at.s1 = slabs;
+  if (splits > 1) {
+    // (a split starts at an even slab: rows come two slabs at a time)
+    const uint32_t pairs = uint32_t((slabs + 1) / 2), q = pairs / splits, r = pairs % splits;
+    at.s0 = 2 * (Int(at.split) * q + (at.split < r ? at.split : r));
+    if (at.split + 1 < splits) at.s1 = at.s0 + 2 * (q + (at.split < r ? 1 : 0));
+  }
+}
+
+constexpr uint32_t kCus = 256;
+
+// Which tile of a product by groups of rows a workgroup makes; false: none. The host
+// knows a bound of the tiles only. Where the full tiles would leave the chip at most
+// half full in their last round, and the small ones find room beside them, those of
+// the last round are made in two halves of 128 rows.
+template <int TM, int COLS>
+__device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int values, int lane,
+                                            Place<kGroupRows>& at, bool& small) {
+  Groups groups;
+  groups.init(p.ends, int(p.batch), int(p.M), lane);
+  const auto rows = groups.tiles<TM>(p.zero_tail);
+  const uint32_t splits = p.splits > 1 ? p.splits : 1;
+  const uint32_t n_full = rows.total * NT * splits, n_small = rows.total_small * NT * splits;
+  uint32_t cut = 0;   // tiles made in halves
+  if (TM == 256 && splits == 1) {
+    const uint32_t last = n_full % kCus;
+    if (last <= kCus / 2 && 2 * last + n_small <= kCus) cut = last;
+  }
+  uint32_t w = blockIdx.x, MT = rows.total, half = 0;
+  small = false;
+  if (w < n_full - cut) {
+    w = xcd_run(w, n_full - cut);
+  } else if (w < n_full - cut + n_small) {
+    w = xcd_run(w - (n_full - cut), n_small);
+    MT = rows.total_small;
+    small = true;
+  } else {
+    w -= n_full - cut + n_small;
+    if (w >= 2 * cut) return false;
+    half = w % 2;
+    w = n_full - cut + w / 2;
+  }
+  at.split = w / (MT * NT);
+  const TileAt t = tile_at(w - at.split * (MT * NT), MT, NT, false);
+  const Group g = small ? groups.find_small<TM>(rows, int(t.mt)) : groups.find<TM>(rows, int(t.mt));
+  at.empty = g.e == int(p.batch);
+  at.b = at.empty ? 0 : g.e;
+  at.m0 = g.at + int(128 * half);
+  at.n0 = int(t.nt * COLS);
+  at.M = g.rows;
+  at.K = at.empty ? 0 : int(p.K);
+  at.d_row = g.start;
+  at.a_off = g.start * p.lda;
+  at.b_off = at.b * p.b_bs;
+  slabs_of(at, values, splits);
+  small = small || blockIdx.x >= n_full - cut;
+  return at.m0 < at.M;
+}
+
+// The tiles of sums by groups that one workgroup makes one after another. A sum is as
+// long as its group has rows, so an XCD that took whole groups would have too much or
+// too little to do (16 groups: 2841 rows in two of them, 2048 in the mean); the groups'
+// units (tiles, times splits) are taken in rounds instead, the largest groups first,
+// and in each round an XCD takes neighbouring units.
+struct SumList {
+  Groups groups;
+  uint32_t MT, NT, units;   // units: of one group
+
+  __device__ __forceinline__ void init(const TileArgs& p, uint32_t MT_, uint32_t NT_, int lane) {
+    groups.init(p.ends, int(p.batch), int(p.K), lane);
+    groups.sort();
+    MT = MT_;
+    NT = NT_;
+    units = MT * NT * (p.splits > 1 ? p.splits : 1);
+  }
+  // The tile of round k; false: none.
+  template <int TM, int COLS>
+  __device__ __forceinline__ bool locate(const TileArgs& p, uint32_t k, int values,
+                                         Place<kGroupSums>& at) const {
+    const uint32_t xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
+    const uint32_t w = k * gridDim.x + xcd * (gridDim.x / kXcds) + i;
+    const uint32_t slot = w / units, u = w - slot * units;
+    if (slot >= uint32_t(groups.E)) return false;
+    at.split = u / (MT * NT);
+    const TileAt t = tile_at(u - at.split * (MT * NT), MT, NT, false);
+    const Group g = groups.sorted(int(slot));
+    at.empty = false;
+    at.b = g.e;
+    at.m0 = int(t.mt * TM);
+    at.n0 = int(t.nt * COLS);
+    at.M = int(p.M);
+    at.K = g.rows;
+    at.d_row = 0;
+    at.a_off = g.start * p.lda;
+    at.b_off = g.start * p.ldb;
+    slabs_of(at, values, p.splits > 1 ? p.splits : 1);
+    return true;
+  }
+};
+
+// The ring's stages in LDS.
+struct Ring {
+  char *b0, *b1, *b2, *b3, *a0, *a1, *a2, *a3;
+};
 
 // 256 rows: one workgroup a CU (a wave's 64 accumulators of 4 floats fill the
 // accumulator registers, so 128 x 128 of D come from 16 fragment reads);
 // 128 x 128: two workgroups a CU.
 //
-// By groups a workgroup finds its tile's group first (about 1 us); workgroups past
-// the last tile, whose number the host only knows a bound of, end there. Rows
-// behind the last group are a group whose sum is empty: its tiles store zeros.
+// Sums by groups: a workgroup a place of the chip makes one tile after another (`list`).
+// It sends the first loads of its next tile before it stores the results of the one
+// just summed, and does not wait for the stores: with sums as short as a group has rows
+// the stores and the ring's first round trip cost as much as the sum (weight gradients
+// of 24576 rows of 64 groups, 2048 x 1408: 242 -> 220 us). The other products gain
+// nothing by it.
 template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
-__global__ __launch_bounds__(kTileWaves* kWave)
-__attribute__((amdgpu_waves_per_eu(TM == 256 ? 1 : 2, TM == 256 ? 1 : 2)))
-void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
+__device__ __forceinline__ void make_tile(const TileArgs& p, Place<GRP> at, const SumList& list,
+                                          const Ring& ring, int lane, int wave) {
   constexpr int kBM = TM / 32, kBN = TN / 32;   // 16-row and 16-column blocks a wave
   constexpr int kCols = EPI == kGated ? TN / 2 : TN;   // columns of D a tile
   static_assert((EPI == kGated) == two_sources(SRCB), "gated: two sources of B");
-  // The ring. Separate objects, so that the compiler can tell the stages apart;
-  // with rows, which come two slabs at a time, A's stages 0 and 1 are one, and 2
-  // and 3.
   constexpr bool kPairs = Loader<SRCA, TM>::kSlabs == 2;
-  __shared__ __attribute__((aligned(1024))) char b0[TN * 64], b1[TN * 64], b2[TN * 64], b3[TN * 64];
-  __shared__ __attribute__((aligned(1024))) char a0[TM * (kPairs ? 128 : 64)],
-      a2[TM * (kPairs ? 128 : 64)], a1[kPairs ? 16 : TM * 64], a3[kPairs ? 16 : TM * 64];
-
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
-  Groups groups;
-  Groups::Tiles<TM> row_tiles;
-  if constexpr (GRP != kWhole)
-    groups.init(p.ends, int(p.batch), int(GRP == kGroupRows ? p.M : p.K), lane);
-  if constexpr (GRP == kGroupRows) {
-    row_tiles = groups.tiles<TM>(p.zero_tail);
-    MT = row_tiles.total;
-    n_tiles = MT * NT;
-  }
-  const uint32_t splits = p.splits > 1 ? p.splits : 1, total = n_tiles * splits;
-  if (GRP == kGroupRows && blockIdx.x >= total) return;
   constexpr int kValues = slab_values(SRCA);
+  constexpr bool kLoop = GRP == kGroupSums;   // one tile after another
+  using Int = typename Place<GRP>::Int;
+  const int wm = wave >> 1, wn = wave & 1, g = lane >> 4;
+  const uint32_t splits = p.splits > 1 ? p.splits : 1;
+  char *const b0 = ring.b0, *const b1 = ring.b1, *const b2 = ring.b2, *const b3 = ring.b3;
+  char *const a0 = ring.a0, *const a1 = ring.a1, *const a2 = ring.a2, *const a3 = ring.a3;
 
   Loader<SRCA, TM> la;
   Loader<SRCB, TN> lb;
   Scales ca, cb0, cb1;
-  uint32_t work, split = 0, slot = 0;
-  if constexpr (GRP == kGroupSums) {
-    n_tiles = MT * NT;   // of a group
-    spread(blockIdx.x, n_tiles * splits, slot, work);
-    if (work >= n_tiles * splits) return;
-  } else {
-    work = xcd_run(blockIdx.x, total);
-  }
-  if (splits > 1) {
-    split = work / n_tiles;
-    work -= split * n_tiles;
-  }
-  TileAt t = tile_at(work, MT, NT, GRP == kWhole && p.batch > 1);
-  int64_t a_off = t.b * p.a_bs, b_off = t.b * p.b_bs;   // elements (4-bit codes: bytes)
-  int64_t d_row = 0;                                    // first row of D of the group
-  bool empty = false;                                   // the tail
-  if constexpr (GRP == kGroupRows) {
-    const Group at = groups.find<TM>(row_tiles, int(t.mt));
-    empty = at.e == int(p.batch);
-    t.b = empty ? 0 : at.e;
-    t.mt = at.tile;
-    a_off = at.start * p.lda;
-    b_off = t.b * p.b_bs;
-    d_row = at.start;
-    p.M = at.rows;
-    if (empty) p.K = p.b_sum = p.b_rows = 0;
-  } else if constexpr (GRP == kGroupSums) {
-    const Group at = groups.large_first(int(slot));
-    t.b = at.e;
-    a_off = at.start * p.lda;
-    b_off = at.start * p.ldb;
-    p.K = at.rows;
-  }
-  const int64_t slabs = (p.K + kValues - 1) / kValues;
-  int64_t s0 = 0, s1 = slabs;   // the slabs to sum
-  if (splits > 1) {
-    // (a split starts at an even slab: rows come two slabs at a time)
-    const uint32_t pairs = uint32_t((slabs + 1) / 2), q = pairs / splits, r = pairs % splits;
-    s0 = 2 * (int64_t(split) * q + (split < r ? split : r));
-    if (split + 1 < splits) s1 = s0 + 2 * (q + (split < r ? 1 : 0));
-  }
-  const int64_t m0 = t.mt * TM, n0 = t.nt * kCols;
-  la.init(p, p.a, nullptr, a_off, p.lda, m0, p.M, s1, lane, wave);
-  lb.init(p, p.b0, p.b1, b_off, p.ldb, n0, p.N, s1, lane, wave);
   if constexpr (DT == kMX4) {
-    ca.init(p.as, t.b * p.as_bs, p.K, m0, p.M);
-    cb0.init(p.bs0, t.b * p.bs_bs, p.K, n0, p.N);
-    if constexpr (EPI == kGated) cb1.init(p.bs1, t.b * p.bs_bs, p.K, n0, p.N);
+    ca.init(p.as, at.b * p.as_bs, p.K, at.m0, p.M);
+    cb0.init(p.bs0, at.b * p.bs_bs, p.K, at.n0, p.N);
+    if constexpr (EPI == kGated) cb1.init(p.bs1, at.b * p.bs_bs, p.K, at.n0, p.N);
   }
   Reader<SRCA> ra;
   Reader<SRCB> rb;
@@ -583,8 +658,12 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   // Fn; loads slab s + 4 to this slab's own stage (ta, tb), whose fragments every
   // wave has read (rows: slabs s + 3 and s + 4 to the stage of s - 1 and s, in
   // odd turns).
-  auto slab = [&](auto turn, int64_t s, const char* na, const char* nb, char* ta, char* tb,
-                  const u32x4 (&Fc)[16], u32x4 (&Fn)[16]) {
+  // Stores of the tile before that this wave has sent at least, after this tile's
+  // first loads. The first two slabs (`first`) wait for loads that were sent before
+  // them and leave the stores in flight.
+  constexpr int kStores = !kLoop ? 0 : EPI == kGated ? kBM * (kBN / 4) : kBM * (kBN / 2);
+  auto slab = [&](auto turn, auto first, Int s, const char* na, const char* nb, char* ta, char* tb,
+                  const u32x4 (&Fc)[16], u32x4 (&Fn)[16]) __attribute__((always_inline)) {
     constexpr int SEL = decltype(turn)::value;
     auto mma = [&](int i) {
       // in blocks of 2 x 2, each MFMA sharing a fragment with the one before: at the
@@ -630,22 +709,42 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     // an odd slab's, before that slab's loads of B, two or one slab ago)
     constexpr int kBefore = kPairs ? kLoadsB : kLoadsA + kLoadsB;
     constexpr int kOpen = kVmem + kBefore + (SEL == 1 && !kPairs ? kWords : 0);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kOpen, 0));
+    constexpr int kWith = kOpen + (decltype(first)::value && SEL < 2 ? kStores : 0);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kWith < 63 ? kWith : 63, 0));
   };
 
   char* const r1 = kPairs ? a0 : a1;
   char* const r3 = kPairs ? a2 : a3;
+  // The loads of a tile's first four slabs.
+  auto begin = [&](const TileArgs& p, const Place<GRP>& q) {
+    TileArgs of = p;
+    of.K = q.K;
+    if (GRP == kGroupRows && q.empty) of.b_sum = of.b_rows = 0;
+    la.init(of, p.a, nullptr, q.a_off, p.lda, q.m0, q.M, q.s1, lane, wave);
+    lb.init(of, p.b0, p.b1, q.b_off, p.ldb, q.n0, p.N, q.s1, lane, wave);
+    issue_a(a0, kPairs ? q.s0 / 2 : q.s0);
+    issue_b(b0, q.s0);
+    if constexpr (!kPairs) issue_a(r1, q.s0 + 1);
+    issue_b(b1, q.s0 + 1);
+    issue_a(a2, kPairs ? q.s0 / 2 + 1 : q.s0 + 2);
+    issue_b(b2, q.s0 + 2);
+    if constexpr (!kPairs) issue_a(r3, q.s0 + 3);
+    issue_b(b3, q.s0 + 3);
+  };
   static_for<0, kWords>([&](auto i) { load_scale(i, 0); });
   __builtin_amdgcn_sched_barrier(0);
-  issue_a(a0, kPairs ? s0 / 2 : s0);
-  issue_b(b0, s0);
-  if constexpr (!kPairs) issue_a(r1, s0 + 1);
-  issue_b(b1, s0 + 1);
-  issue_a(a2, kPairs ? s0 / 2 + 1 : s0 + 2);
-  issue_b(b2, s0 + 2);
-  if constexpr (!kPairs) issue_a(r3, s0 + 3);
-  issue_b(b3, s0 + 3);
+  begin(p, at);
   take_scales();
+  if constexpr (kLoop) {
+    // As many stores to nowhere as a tile before would have sent at least: the waits of
+    // every tile count the same.
+    const auto nowhere = buffer(nullptr, 0);
+#pragma unroll
+    for (int i = 0; i < kStores; ++i)   // (at different places, so that none is left out)
+      __builtin_amdgcn_raw_buffer_store_b32(0u, nowhere, kOutOfRange - 16 * i, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  for (uint32_t tile = 0;; ++tile) {
   // Pinned to accumulator registers one by one: equal starting values would be
   // merged, and the loop would then copy them.
 #pragma unroll
@@ -658,48 +757,89 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     }
   settle();
   // slabs 0 and 1 landed (after them: rows, one round of A and two of B)
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm((kPairs ? 1 : 2) * kLoadsA + 2 * kLoadsB, 15));
+  constexpr int kFirst = (kPairs ? 1 : 2) * kLoadsA + 2 * kLoadsB + kStores;
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(kFirst < 63 ? kFirst : 63, 15));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  if constexpr (kLoop) {
+    ra.renew();
+    rb.renew();
+  }
 #pragma unroll
   for (int i = 0; i < kBM + kBN; ++i) read(a0, 0, b0, F0, i);
   __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-  for (int64_t s = s0; s < s1; s += 4) {
-    slab(std::integral_constant<int, 0>{}, s + 0, r1, b1, a0, b0, F0, F1);
-    slab(std::integral_constant<int, 1>{}, s + 1, a2, b2, r1, b1, F1, F0);
-    slab(std::integral_constant<int, 2>{}, s + 2, r3, b3, a2, b2, F0, F1);
-    slab(std::integral_constant<int, 3>{}, s + 3, a0, b0, r3, b3, F1, F0);
+  // One turn of the ring, or its first half.
+  auto turn = [&](auto first, auto half, Int s) __attribute__((always_inline)) {
+    if constexpr (kLoop) {
+      ra.renew();
+      rb.renew();
+    }
+    slab(std::integral_constant<int, 0>{}, first, s + 0, r1, b1, a0, b0, F0, F1);
+    slab(std::integral_constant<int, 1>{}, first, s + 1, a2, b2, r1, b1, F1, F0);
+    if constexpr (!decltype(half)::value) {
+      slab(std::integral_constant<int, 2>{}, first, s + 2, r3, b3, a2, b2, F0, F1);
+      slab(std::integral_constant<int, 3>{}, first, s + 3, a0, b0, r3, b3, F1, F0);
+    }
     take_scales();
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  if constexpr (kLoop) {
+    // (after the first turn: where two slabs are left or one, no two of zeros besides)
+    Int s = at.s0;
+    turn(yes, no, s);
+    for (s += 4; s + 2 < at.s1; s += 4) turn(no, no, s);
+    if (s < at.s1) turn(no, yes, s);
+  } else {
+    for (Int s = at.s0; s < at.s1; s += 4) turn(no, no, s);
   }
-  // No load may still be writing LDS when the workgroup ends.
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
-  settle();
-#pragma unroll
-  for (int i = 0; i < kBM; ++i)
-#pragma unroll
-    for (int j = 0; j < kBN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read from here on only
-  const int64_t row = m0 + 16 * kBM * wm, col = n0 + (EPI == kGated ? 8 : 16) * kBN * wn;
+  Place<GRP> next;
+  bool more = false;
+  auto finish = [&](const TileArgs& p) {
+  const int64_t row = at.m0 + 16 * kBM * wm, col = at.n0 + (EPI == kGated ? 8 : 16) * kBN * wn;
   // 8-bit integers: the scales of this lane's rows, and of its columns of each block
   float scale_a[8];
   f32x4 scale_b[8];
   if constexpr (DT == kI8) {
-    const int64_t left = empty || p.M < row ? 0 : p.M - row, cols = empty || p.N < col ? 0 : p.N - col;
-    const auto sa = buffer(p.sa + (GRP == kGroupRows ? d_row : t.b * p.M) + row,
+    const int64_t left = at.empty || at.M < row ? 0 : at.M - row;
+    const int64_t cols = at.empty || p.N < col ? 0 : p.N - col;
+    const auto sa = buffer(p.sa + (GRP == kGroupRows ? at.d_row : at.b * p.M) + row,
                            uint32_t(left < 16 * kBM ? left : 16 * kBM) * 4);
     const uint32_t bytes = uint32_t(cols < 16 * kBN ? cols : 16 * kBN) * 4;
-    const auto sb0 = buffer(p.sb0 + t.b * p.N + col, bytes);
-    const auto sb1 = buffer((EPI == kGated ? p.sb1 : p.sb0) + t.b * p.N + col, bytes);
+    const auto sb0 = buffer(p.sb0 + at.b * p.N + col, bytes);
+    const auto sb1 = buffer((EPI == kGated ? p.sb1 : p.sb0) + at.b * p.N + col, bytes);
 #pragma unroll
     for (int i = 0; i < kBM; ++i)
       scale_a[i] = __builtin_bit_cast(
           float, __builtin_amdgcn_raw_buffer_load_b32(sa, 64 * i + 4 * (lane & 15), 0, 0));
 #pragma unroll
     for (int j = 0; j < kBN; ++j) {
-      const int at = EPI == kGated ? 64 * (j >> 1) + 16 * g : 64 * j + 16 * g;
+      const int c = EPI == kGated ? 64 * (j >> 1) + 16 * g : 64 * j + 16 * g;
       scale_b[j] = __builtin_bit_cast(
-          f32x4, __builtin_amdgcn_raw_buffer_load_b128(EPI == kGated && (j & 1) ? sb1 : sb0, at, 0, 0));
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(EPI == kGated && (j & 1) ? sb1 : sb0, c, 0, 0));
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
+  if constexpr (kLoop) {
+    // The ring is free when every wave has read its last fragments; the zeros loaded past
+    // the sum's end have long landed. (The compiler counts loads and stores along every
+    // path it sees: no load may be open on one that skips the next ones, and every path
+    // has to store as often.)
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+    more = list.template locate<TM, kCols>(p, tile + 1, kValues, next);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (more) begin(p, next);
+    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    // No load may still be writing LDS when the workgroup ends.
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
+  }
+  settle();
+#pragma unroll
+  for (int i = 0; i < kBM; ++i)
+#pragma unroll
+    for (int j = 0; j < kBN; ++j) asm volatile("" : "+a"(acc[i][j]));   // read from here on only
   // The sums of block (i, j); 8-bit integers: those values times the scales.
   auto sums = [&](int i, int j) {
     if constexpr (DT == kI8) {
@@ -711,6 +851,8 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
         r[e] = float(__builtin_bit_cast(int, x)) * scale_a[i] * scale_b[j][e];
       }
       return r;
+    } else if constexpr (GRP != kWhole) {
+      return sum(acc[i][j]);
     } else {
       return acc[i][j];
     }
@@ -720,6 +862,19 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   const bool wide = EPI == kStore && (any_output(DT) ? p.out_type == BMM_ELEM_F32 : splits > 1);
   // (192 columns: 48 of H a wave, the last 16 by themselves)
   constexpr bool kLast = EPI == kGated && kBN % 4 != 0;
+  constexpr int kAux = GRP == kWhole ? kNonTemporal : 0;
+  // Offsets of this lane's columns in the first 16 rows; those outside are past
+  // every buffer's end.
+  const int64_t ld = EPI == kStore && splits > 1 ? p.N : p.ldd;
+  const uint32_t row_bytes = uint32_t(ld) * (wide ? 4 : 2), step = 16 * row_bytes;
+  uint32_t off[8];
+  auto offsets = [&]() {
+#pragma unroll
+    for (int j = 0; j < (wide ? kBN : kPairsN); ++j) {
+      const int c = wide ? 16 * j + 4 * g : 32 * j + 16 * (g & 1) + 8 * (g >> 1);
+      off[j] = col + c < p.N ? (lane & 15) * row_bytes + (wide ? 4 : 2) * c : kOutOfRange;
+    }
+  };
   u32x4 out[8][2];
   u32x2 last[8];
   if constexpr (EPI == kGated) {
@@ -749,54 +904,42 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
     }
   }
 
-  // Offsets of this lane's columns in the first 16 rows; those outside are past
-  // every buffer's end.
-  const int64_t ld = EPI == kStore && splits > 1 ? p.N : p.ldd;
-  const uint32_t row_bytes = uint32_t(ld) * (wide ? 4 : 2), step = 16 * row_bytes;
-  uint32_t at[8];
-  auto offsets = [&]() {
-#pragma unroll
-    for (int j = 0; j < (wide ? kBN : kPairsN); ++j) {
-      const int c = wide ? 16 * j + 4 * g : 32 * j + 16 * (g & 1) + 8 * (g >> 1);
-      at[j] = col + c < p.N ? (lane & 15) * row_bytes + (wide ? 4 : 2) * c : kOutOfRange;
-    }
-  };
   if constexpr (EPI == kGated) {
     auto store = [&](void* d, auto value, auto last_value) {
       const auto to = out_rows(static_cast<uint16_t*>(d) +
-                                   ((GRP == kGroupRows ? d_row : t.b * p.M) + row) * ld + col,
-                               row_bytes, p.M - row, 16 * kBM);
+                                   ((GRP == kGroupRows ? at.d_row : at.b * p.M) + row) * ld + col,
+                               row_bytes, at.M - row, 16 * kBM);
       offsets();
 #pragma unroll
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(value(i, j), to, at[j] + i * step, 0, kNonTemporal);
+          __builtin_amdgcn_raw_buffer_store_b128(value(i, j), to, off[j] + i * step, 0, kAux);
       if constexpr (kLast) {
         const int c = 32 * kPairsN + 4 * g;
-        const uint32_t at_last = col + c < p.N ? (lane & 15) * row_bytes + 2 * c : kOutOfRange;
+        const uint32_t off_last = col + c < p.N ? (lane & 15) * row_bytes + 2 * c : kOutOfRange;
 #pragma unroll
         for (int i = 0; i < kBM; ++i)
-          __builtin_amdgcn_raw_buffer_store_b64(last_value(i), to, at_last + i * step, 0, kNonTemporal);
+          __builtin_amdgcn_raw_buffer_store_b64(last_value(i), to, off_last + i * step, 0, kAux);
       }
     };
     store(p.d, [&](int i, int j) { return out[i][j]; }, [&](int i) { return last[i]; });
     if constexpr (!any_output(DT)) {
       if (p.d1) {
-        store(p.d1, [&](int i, int j) { return join16<DT>(acc[i][4 * j], acc[i][4 * j + 2]); },
-              [&](int i) { return pack4<DT>(acc[i][kBN - 2]); });
-        store(p.d2, [&](int i, int j) { return join16<DT>(acc[i][4 * j + 1], acc[i][4 * j + 3]); },
-              [&](int i) { return pack4<DT>(acc[i][kBN - 1]); });
+        store(p.d1, [&](int i, int j) { return join16<DT>(sums(i, 4 * j), sums(i, 4 * j + 2)); },
+              [&](int i) { return pack4<DT>(sums(i, kBN - 2)); });
+        store(p.d2, [&](int i, int j) { return join16<DT>(sums(i, 4 * j + 1), sums(i, 4 * j + 3)); },
+              [&](int i) { return pack4<DT>(sums(i, kBN - 1)); });
       }
     }
   } else {
     // Rows below rows0 go to d, those from row1 (a multiple of 16) on to d1.
     const int size = wide ? 4 : 2;
     const bool parts = splits > 1;
-    const char* d = parts ? reinterpret_cast<char*>(p.part + split * p.part_floats)
+    const char* d = parts ? reinterpret_cast<char*>(p.part + at.split * p.part_floats)
                           : static_cast<char*>(p.d);
-    const int64_t rows = GRP == kGroupRows || parts ? p.M : p.rows0;
-    const auto to = out_rows(d + (((GRP == kGroupRows ? d_row : t.b * rows) + row) * ld + col) * size,
+    const int64_t rows = GRP == kGroupRows || parts ? at.M : p.rows0;
+    const auto to = out_rows(d + (((GRP == kGroupRows ? at.d_row : at.b * rows) + row) * ld + col) * size,
                              row_bytes, rows - row, 16 * kBM);
     auto to1 = to;
     int second = kBM;   // first block of 16 rows that goes to d1
@@ -804,14 +947,14 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
       if (!parts && row + 16 * kBM > p.row1) {
         second = row < p.row1 ? int(p.row1 - row) / 16 : 0;
         to1 = out_rows(static_cast<char*>(p.d1) +
-                           ((t.b * rows + row - p.row1) * ld + col) * size,
+                           ((at.b * rows + row - p.row1) * ld + col) * size,
                        row_bytes, p.row1 + rows - row, 16 * kBM);
       }
     }
     offsets();
     auto store = [&](int i, int j, u32x4 v, auto nt) {
       __builtin_amdgcn_raw_buffer_store_b128(v, SRCA == kTrans && i >= second ? to1 : to,
-                                             at[j] + i * step, 0, decltype(nt)::value);
+                                             off[j] + i * step, 0, decltype(nt)::value);
     };
     float rescale = 1.f;
     if constexpr (DT == kF16) rescale = p.rescale ? *p.rescale : 1.f;
@@ -826,7 +969,7 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j)
           store(i, j, join16<decltype(type)::value>(result(i, 2 * j), result(i, 2 * j + 1)),
-                std::integral_constant<int, kNonTemporal>{});
+                std::integral_constant<int, kAux>{});
     };
     auto store32 = [&](auto nt) {
 #pragma unroll
@@ -834,15 +977,111 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
 #pragma unroll
         for (int j = 0; j < kBN; ++j) store(i, j, __builtin_bit_cast(u32x4, sums(i, j)), nt);
     };
-    if constexpr (!any_output(DT)) {
+    if constexpr (kLoop) {
+      // Two neighbouring blocks in one store of 16 bits a value, or the first of them in
+      // float32 and the second later.
+      if (wide) rescale = 1.f;   // (the join applies it)
+      uint32_t later[4];
+#pragma unroll
+      for (int j = 0; j < kPairsN; ++j) {
+        const int c = 32 * j + 4 * g;
+        later[j] = col + c + 16 < p.N ? (lane & 15) * row_bytes + 4 * (c + 16) : kOutOfRange;
+        if (wide) off[j] = col + c < p.N ? (lane & 15) * row_bytes + 4 * c : kOutOfRange;
+      }
+      constexpr int kType = any_output(DT) ? kBF16 : DT;
+      const bool f16 = any_output(DT) && p.out_type == BMM_ELEM_F16;
+#pragma unroll
+      for (int i = 0; i < kBM; ++i)
+#pragma unroll
+        for (int j = 0; j < kPairsN; ++j) {
+          const f32x4 x = result(i, 2 * j), y = result(i, 2 * j + 1);
+          u32x4 v = join16<kType>(x, y);
+          if constexpr (any_output(DT)) {
+            const u32x4 h = join16<kF16>(x, y);
+            v = f16 ? h : v;
+          }
+          store(i, j, wide ? __builtin_bit_cast(u32x4, x) : v, std::integral_constant<int, kAux>{});
+        }
+      if (wide) {
+#pragma unroll
+        for (int j = 0; j < kPairsN; ++j) off[j] = later[j];
+#pragma unroll
+        for (int i = 0; i < kBM; ++i)
+#pragma unroll
+          for (int j = 0; j < kPairsN; ++j)
+            store(i, j, __builtin_bit_cast(u32x4, result(i, 2 * j + 1)),
+                  std::integral_constant<int, kAux>{});
+      }
+    } else if constexpr (!any_output(DT)) {
       if (wide) store32(std::integral_constant<int, 0>{});
       else store16(std::integral_constant<int, DT>{});
     } else {
-      if (wide) store32(std::integral_constant<int, kNonTemporal>{});
+      if (wide) store32(std::integral_constant<int, kAux>{});
       else if (p.out_type == BMM_ELEM_BF16) store16(std::integral_constant<int, kBF16>{});
       else store16(std::integral_constant<int, kF16>{});
     }
   }
+  };
+  if constexpr (GRP != kWhole) finish(args_again());
+  else finish(p);
+  if (!more) break;
+  at = next;
+  }
+}
+
+// A workgroup a tile, or by groups of the summed rows a workgroup a place of the chip.
+template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
+__global__ __launch_bounds__(kTileWaves* kWave)
+__attribute__((amdgpu_waves_per_eu(TM == 256 ? 1 : 2, TM == 256 ? 1 : 2)))
+void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
+  constexpr int kCols = EPI == kGated ? TN / 2 : TN;
+  // The ring. Separate objects, so that the compiler can tell the stages apart;
+  // with rows, which come two slabs at a time, A's stages 0 and 1 are one, and 2
+  // and 3.
+  constexpr bool kPairs = Loader<SRCA, TM>::kSlabs == 2;
+  __shared__ __attribute__((aligned(1024))) char b0[TN * 64], b1[TN * 64], b2[TN * 64], b3[TN * 64];
+  __shared__ __attribute__((aligned(1024))) char a0[TM * (kPairs ? 128 : 64)],
+      a2[TM * (kPairs ? 128 : 64)], a1[kPairs ? 16 : TM * 64], a3[kPairs ? 16 : TM * 64];
+  const Ring ring{b0, b1, b2, b3, a0, a1, a2, a3};
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  constexpr int kValues = slab_values(SRCA);
+  Place<GRP> at;
+  SumList list;
+  if constexpr (GRP == kGroupSums) {
+    list.init(p, MT, NT, lane);
+    if (!list.template locate<TM, kCols>(p, 0, kValues, at)) return;
+  } else if constexpr (GRP == kGroupRows) {
+    bool small;
+    if (!locate_rows<TM, kCols>(p, NT, kValues, lane, at, small)) return;
+    if constexpr (TM == 256) {
+      if (small) {
+        make_tile<DT, SRCA, SRCB, EPI, GRP, 128, TN>(p, at, list, ring, lane, wave);
+        return;
+      }
+    }
+  } else {
+    const uint32_t splits = p.splits > 1 ? p.splits : 1;
+    uint32_t work = xcd_run(blockIdx.x, n_tiles * splits);
+    at.split = 0;
+    if (splits > 1) {
+      at.split = work / n_tiles;
+      work -= at.split * n_tiles;
+    }
+    const TileAt t = tile_at(work, MT, NT, p.batch > 1);
+    at.b = t.b;
+    at.m0 = t.mt * TM;
+    at.n0 = t.nt * kCols;
+    at.M = p.M;
+    at.K = p.K;
+    at.a_off = t.b * p.a_bs;
+    at.b_off = t.b * p.b_bs;
+    at.d_row = 0;
+    at.empty = false;
+    slabs_of(at, kValues, splits);
+  }
+  make_tile<DT, SRCA, SRCB, EPI, GRP, TM, TN>(p, at, list, ring, lane, wave);
 }
 
 template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
@@ -856,8 +1095,13 @@ hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
   if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37)
     return hipErrorInvalidConfiguration;
   auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, GRP, TM, TN>;
-  const int64_t grid = GRP == kGroupSums ? p.batch * spread_units(uint32_t(MT * NT * splits))
-                                         : n * splits;
+  int64_t grid = n * splits;
+  if (GRP == kGroupRows && TM == 256 && splits == 1) grid += kCus / 2;   // (tiles in halves)
+  if (GRP == kGroupSums) {   // one for each that the chip holds at once, an equal number a XCD
+    constexpr int64_t kPlaces = kCus * (TM == 128 ? 2 : 1);
+    grid = (grid + kXcds - 1) / kXcds * kXcds;
+    grid = grid < kPlaces ? grid : kPlaces;
+  }
   if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kTileWaves * kWave), 0, s, p, uint32_t(n),
                      uint32_t(MT), uint32_t(NT));
