@@ -11,9 +11,11 @@ using bmm::report;
 
 // Layout of the backward passes' workspace: for the gated block as bmm_gated_backward's
 // ([dG | dU], the factor that undoes their scaling, the peaks), then from slopes_bytes
-// on the partial sums of one product at a time.
+// on the partial sums of one product at a time, or where both products are made in one
+// launch of dX and from dw_parts on of dW.
 struct GradPlan {
-  int64_t dgu_bytes = 0, slopes_bytes = 0, need = 0;
+  int64_t dgu_bytes = 0, slopes_bytes = 0, dw_parts = 0, need = 0;
+  bool both = false;  // in one launch
   int64_t sum = 0;    // values that dX sums: N, or both halves of [dG | dU]
   bmm::TilePlan dx, dw;
 };
@@ -30,11 +32,12 @@ GradPlan plan_grads(const bmm_grouped_desc& d, bool gated) {
   p.dx = bmm::plan_group_rows(d.groups, d.T, d.K, (p.sum + 31) / 32, true);
   // (slabs of the mean group)
   p.dw = bmm::plan_tiles(d.groups, p.sum, d.K, (d.T + 32 * d.groups - 1) / (32 * d.groups), true);
-  const int64_t parts[] = {p.dx.splits > 1 ? p.dx.splits * d.T * d.K * 4 : 0,
-                           p.dw.splits > 1 ? p.dw.splits * d.groups * p.sum * d.K * 4 : 0};
-  p.need = p.slopes_bytes;
-  for (int64_t n : parts)
-    if (p.slopes_bytes + n > p.need) p.need = p.slopes_bytes + n;
+  p.both = p.dx.tile == bmm::kTile128 && p.dw.tile == bmm::kTile128;
+  const int64_t dx = p.dx.splits > 1 ? p.dx.splits * d.T * d.K * 4 : 0;
+  const int64_t dw = p.dw.splits > 1 ? p.dw.splits * d.groups * p.sum * d.K * 4 : 0;
+  p.dw_parts = p.slopes_bytes + (p.both ? (dx + 255) / 256 * 256 : 0);
+  p.need = p.slopes_bytes + dx;
+  if (p.dw_parts + dw > p.need) p.need = p.dw_parts + dw;
   return p;
 }
 
@@ -98,7 +101,7 @@ int grouped_backward(const bmm::GroupedGrads& g, const int32_t* ends, const bmm_
   if (!st.ok()) return report(st);
   if (d.K == 0 || (d.T == 0 && d.N == 0)) return report(st);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.slopes_bytes);
+  char* const parts = static_cast<char*>(workspace);
   // what the products take: dY, or [dG | dU] in the workspace
   const uint16_t* dy = g.dY;
   int64_t ld = d.ld_y;
@@ -118,48 +121,48 @@ int grouped_backward(const bmm::GroupedGrads& g, const int32_t* ends, const bmm_
     dy = dgu;
     ld = plan.sum;
   }
-  if (g.dX && d.T > 0) {
-    bmm::TileArgs a = group_args(d, ends);
-    a.a = dy;
-    a.b0 = g.W;
-    a.b1 = gated ? g.W1 : g.W;
-    a.d = const_cast<uint16_t*>(g.dX);
-    a.M = a.rows0 = d.T;
-    a.N = a.ldd = d.K;
-    a.K = plan.sum;
-    a.lda = ld;
-    a.b_bs = d.N * d.K;
-    a.b_sum = bmm::padded_width(d.N);
-    a.b_rows = d.N;
-    a.tile = plan.dx.tile;
-    a.splits = plan.dx.splits;
-    a.part = part;
-    a.part_floats = d.T * d.K;
-    a.rescale = rescale;
-    const int rc = hip_status(bmm::launch_grouped_dx(a, d.dtype, s), "grouped dX launch");
+  bmm::TileArgs dx = group_args(d, ends), dw = dx;
+  const bool want_dx = g.dX && d.T > 0, want_dw = g.dW && d.N > 0;
+  dx.a = dy;
+  dx.b0 = g.W;
+  dx.b1 = gated ? g.W1 : g.W;
+  dx.d = const_cast<uint16_t*>(g.dX);
+  dx.M = dx.rows0 = d.T;
+  dx.N = dx.ldd = d.K;
+  dx.K = plan.sum;
+  dx.lda = ld;
+  dx.b_bs = d.N * d.K;
+  dx.b_sum = bmm::padded_width(d.N);
+  dx.b_rows = d.N;
+  dx.tile = plan.dx.tile;
+  dx.splits = plan.dx.splits;
+  dx.part = reinterpret_cast<float*>(parts + plan.slopes_bytes);
+  dx.part_floats = d.T * d.K;
+  dx.rescale = rescale;
+  dw.a = dy;
+  dw.b0 = g.X;
+  dw.d = const_cast<uint16_t*>(g.dW);
+  dw.d1 = const_cast<uint16_t*>(g.dW1);
+  dw.M = plan.sum;
+  dw.lda = ld;
+  dw.rows0 = d.N;
+  if (gated) dw.row1 = bmm::padded_width(d.N);
+  dw.N = dw.ldd = d.K;
+  dw.K = d.T;
+  dw.ldb = d.ld_x;
+  dw.tile = plan.dw.tile;
+  dw.splits = plan.dw.splits;
+  dw.part = reinterpret_cast<float*>(parts + plan.dw_parts);
+  dw.part_floats = d.groups * plan.sum * d.K;
+  dw.rescale = rescale;
+  if (plan.both && want_dx && want_dw)
+    return hip_status(bmm::launch_grouped_both(dx, dw, d.dtype, s), "grouped gradients launch");
+  if (want_dx) {
+    const int rc = hip_status(bmm::launch_grouped_dx(dx, d.dtype, s), "grouped dX launch");
     if (rc != BMM_OK) return rc;
   }
-  if (g.dW && d.N > 0) {
-    bmm::TileArgs a = group_args(d, ends);
-    a.a = dy;
-    a.b0 = g.X;
-    a.d = const_cast<uint16_t*>(g.dW);
-    a.d1 = const_cast<uint16_t*>(g.dW1);
-    a.M = plan.sum;
-    a.lda = ld;
-    a.rows0 = d.N;
-    if (gated) a.row1 = bmm::padded_width(d.N);
-    a.N = a.ldd = d.K;
-    a.K = d.T;
-    a.ldb = d.ld_x;
-    a.tile = plan.dw.tile;
-    a.splits = plan.dw.splits;
-    a.part = part;
-    a.part_floats = d.groups * plan.sum * d.K;
-    a.rescale = rescale;
-    return hip_status(bmm::launch_grouped_dw(a, d.dtype, s), "grouped dW launch");
-  }
-  return BMM_OK;
+  if (want_dw) return hip_status(bmm::launch_grouped_dw(dw, d.dtype, s), "grouped dW launch");
+  return report(st);
 }
 
 // groups 0: one weight for every batch.

@@ -87,6 +87,8 @@ hipError_t launch_grouped_mma(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_grouped_gated(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_grouped_dx(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s);
+// Both in one launch; each by tiles of 128 x 128.
+hipError_t launch_grouped_both(const TileArgs& dx, const TileArgs& dw, int dtype, hipStream_t s);
 hipError_t launch_i8_quantize(int8_t* codes, float* scales, const void* src, int64_t rows, int64_t K,
                               int64_t ld, int elem_type, hipStream_t s);
 // a.ends: by groups, or null.

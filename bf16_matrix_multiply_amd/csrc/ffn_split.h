@@ -50,6 +50,53 @@ hipError_t join(const TileArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Both gradients of a product by groups in one launch, for products so small that
+// either leaves most of the chip idle: workgroups below n_dx make tiles of dX, the
+// others of dW. (777 rows of 5 groups, 528 -> 1000: 14 and 7 us one after the other.)
+template <int DT>
+__global__ __launch_bounds__(kTileWaves* kWave) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void grads_kernel(TileArgs dx, TileArgs dw, uint32_t n_dx, uint32_t NT_dx, uint32_t n_dw,
+                  uint32_t MT_dw, uint32_t NT_dw) {
+  constexpr int kSide = 128;
+  __shared__ __attribute__((aligned(1024))) char b0[kSide * 64], b1[kSide * 64], b2[kSide * 64],
+      b3[kSide * 64], a0[kSide * 128], a1[kSide * 64], a2[kSide * 128], a3[kSide * 64];
+  const Ring ring{b0, b1, b2, b3, a0, a1, a2, a3};
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  SumList list;
+  if (blockIdx.x < n_dx) {
+    Place<kGroupRows> at;
+    bool small;
+    if (!locate_rows<kSide, kSide>(dx, blockIdx.x, NT_dx, 32, lane, at, small)) return;
+    make_tile<DT, kRows, kPackedT2, kStore, kGroupRows, kSide, kSide, 0>(dx, at, list, ring, lane,
+                                                                        wave);
+  } else {
+    Place<kGroupSums> at;
+    list.init(dw, blockIdx.x - n_dx, n_dw, MT_dw, NT_dw, lane);
+    if (!list.template locate<kSide, kSide>(dw, 0, 32, at)) return;
+    make_tile<DT, kTrans, kTrans, kStore, kGroupSums, kSide, kSide, 1>(dw, at, list, ring, lane,
+                                                                      wave);
+  }
+}
+
+template <int DT>
+hipError_t both_gradients(const TileArgs& dx, const TileArgs& dw, hipStream_t s) {
+  const int64_t MT = (dw.M + 127) / 128, NT_dx = (dx.N + 127) / 128, NT_dw = (dw.N + 127) / 128;
+  int64_t n_dx = tile_grid<kGroupRows, 128>(dx, most_row_tiles(dx.M, dx.batch, 128), NT_dx);
+  const int64_t n_dw = tile_grid<kGroupSums, 128>(dw, MT, NT_dw);
+  if (n_dx < 0 || n_dw < 0) return hipErrorInvalidConfiguration;
+  n_dx = (n_dx + kXcds - 1) / kXcds * kXcds;
+  if (n_dx + n_dw > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (n_dx + n_dw == 0) return hipSuccess;
+  hipLaunchKernelGGL(grads_kernel<DT>, dim3(unsigned(n_dx + n_dw)), dim3(kTileWaves * kWave), 0, s,
+                     dx, dw, uint32_t(n_dx), uint32_t(NT_dx), uint32_t(n_dw), uint32_t(MT),
+                     uint32_t(NT_dw));
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && dx.splits > 1) e = join<DT, kGroupRows>(dx, s);
+  if (e == hipSuccess && dw.splits > 1) e = join<DT, kGroupSums>(dw, s);
+  return e;
+}
+
 template <int DT, int SRCA, int SRCB, int GRP = kWhole>
 hipError_t product(const TileArgs& a, hipStream_t s) {
   hipError_t e = launch_tile<DT, SRCA, SRCB, kStore, GRP>(a, s);

@@ -444,10 +444,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t out_rows(const void* d, int64_
 // groups gated 2048 -> 1408, projections kept, 358 us against 370.
 constexpr int kNonTemporal = 2;
 
-// The kernel's arguments, read again: what a loop over tiles needs of them only
-// between two sums would otherwise be kept in (spilled) scalar registers.
+// The kernel's I-th argument (it and those before are TileArgs), read again: what is
+// needed of it only after a sum would otherwise be kept in (spilled) scalar registers.
+template <int I>
 __device__ __forceinline__ const TileArgs& args_again() {
-  uint64_t at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+  uint64_t at = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr()) +
+                I * sizeof(TileArgs);
   asm volatile("" : "+s"(at));
   return *(const TileArgs*)reinterpret_cast<const __attribute__((address_space(4))) TileArgs*>(at);
 }
@@ -484,13 +486,13 @@ __device__ __forceinline__ void slabs_of(Place<GRP>& at, int values, uint32_t sp
 
 constexpr uint32_t kCus = 256;
 
-// Which tile of a product by groups of rows a workgroup makes; false: none. The host
+// Which tile of a product by groups of rows workgroup w makes; false: none. The host
 // knows a bound of the tiles only. Where the full tiles would leave the chip at most
 // half full in their last round, and the small ones find room beside them, those of
 // the last round are made in two halves of 128 rows.
 template <int TM, int COLS>
-__device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int values, int lane,
-                                            Place<kGroupRows>& at, bool& small) {
+__device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint32_t NT, int values,
+                                            int lane, Place<kGroupRows>& at, bool& small) {
   Groups groups;
   groups.init(p.ends, int(p.batch), int(p.M), lane);
   const auto rows = groups.tiles<TM>(p.zero_tail);
@@ -501,14 +503,15 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int 
     const uint32_t last = n_full % kCus;
     if (last <= kCus / 2 && 2 * last + n_small <= kCus) cut = last;
   }
-  uint32_t w = blockIdx.x, MT = rows.total, half = 0;
-  small = false;
+  uint32_t MT = rows.total, half = 0;
+  small = w >= n_full - cut;   // the body for 128 rows
+  bool last = false;           // a small tile
   if (w < n_full - cut) {
     w = xcd_run(w, n_full - cut);
   } else if (w < n_full - cut + n_small) {
     w = xcd_run(w - (n_full - cut), n_small);
     MT = rows.total_small;
-    small = true;
+    last = true;
   } else {
     w -= n_full - cut + n_small;
     if (w >= 2 * cut) return false;
@@ -517,7 +520,7 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int 
   }
   at.split = w / (MT * NT);
   const TileAt t = tile_at(w - at.split * (MT * NT), MT, NT, false);
-  const Group g = small ? groups.find_small<TM>(rows, int(t.mt)) : groups.find<TM>(rows, int(t.mt));
+  const Group g = last ? groups.find_small<TM>(rows, int(t.mt)) : groups.find<TM>(rows, int(t.mt));
   at.empty = g.e == int(p.batch);
   at.b = at.empty ? 0 : g.e;
   at.m0 = g.at + int(128 * half);
@@ -528,7 +531,6 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int 
   at.a_off = g.start * p.lda;
   at.b_off = at.b * p.b_bs;
   slabs_of(at, values, splits);
-  small = small || blockIdx.x >= n_full - cut;
   return at.m0 < at.M;
 }
 
@@ -540,8 +542,12 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t NT, int 
 struct SumList {
   Groups groups;
   uint32_t MT, NT, units;   // units: of one group
+  uint32_t wg, n_wg;        // this workgroup, of so many (a multiple of the XCDs)
 
-  __device__ __forceinline__ void init(const TileArgs& p, uint32_t MT_, uint32_t NT_, int lane) {
+  __device__ __forceinline__ void init(const TileArgs& p, uint32_t wg_, uint32_t n_wg_, uint32_t MT_,
+                                       uint32_t NT_, int lane) {
+    wg = wg_;
+    n_wg = n_wg_;
     groups.init(p.ends, int(p.batch), int(p.K), lane);
     groups.sort();
     MT = MT_;
@@ -552,8 +558,7 @@ struct SumList {
   template <int TM, int COLS>
   __device__ __forceinline__ bool locate(const TileArgs& p, uint32_t k, int values,
                                          Place<kGroupSums>& at) const {
-    const uint32_t xcd = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
-    const uint32_t w = k * gridDim.x + xcd * (gridDim.x / kXcds) + i;
+    const uint32_t w = k * n_wg + wg % kXcds * (n_wg / kXcds) + wg / kXcds;
     const uint32_t slot = w / units, u = w - slot * units;
     if (slot >= uint32_t(groups.E)) return false;
     at.split = u / (MT * NT);
@@ -588,7 +593,9 @@ struct Ring {
 // the stores and the ring's first round trip cost as much as the sum (weight gradients
 // of 24576 rows of 64 groups, 2048 x 1408: 242 -> 220 us). The other products gain
 // nothing by it.
-template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
+//
+// p is the kernel's ARG-th argument.
+template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN, int ARG = 0>
 __device__ __forceinline__ void make_tile(const TileArgs& p, Place<GRP> at, const SumList& list,
                                           const Ring& ring, int lane, int wave) {
   constexpr int kBM = TM / 32, kBN = TN / 32;   // 16-row and 16-column blocks a wave
@@ -1022,7 +1029,7 @@ __device__ __forceinline__ void make_tile(const TileArgs& p, Place<GRP> at, cons
     }
   }
   };
-  if constexpr (GRP != kWhole) finish(args_again());
+  if constexpr (GRP != kWhole) finish(args_again<ARG>());
   else finish(p);
   if (!more) break;
   at = next;
@@ -1050,11 +1057,11 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   Place<GRP> at;
   SumList list;
   if constexpr (GRP == kGroupSums) {
-    list.init(p, MT, NT, lane);
+    list.init(p, blockIdx.x, gridDim.x, MT, NT, lane);
     if (!list.template locate<TM, kCols>(p, 0, kValues, at)) return;
   } else if constexpr (GRP == kGroupRows) {
     bool small;
-    if (!locate_rows<TM, kCols>(p, NT, kValues, lane, at, small)) return;
+    if (!locate_rows<TM, kCols>(p, blockIdx.x, NT, kValues, lane, at, small)) return;
     if constexpr (TM == 256) {
       if (small) {
         make_tile<DT, SRCA, SRCB, EPI, GRP, 128, TN>(p, at, list, ring, lane, wave);
@@ -1084,27 +1091,33 @@ void ffn_tile_kernel(TileArgs p, uint32_t n_tiles, uint32_t MT, uint32_t NT) {
   make_tile<DT, SRCA, SRCB, EPI, GRP, TM, TN>(p, at, list, ring, lane, wave);
 }
 
-template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
-hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
-  const int64_t cols = EPI == kGated ? TN / 2 : TN;
-  const int64_t MT = GRP == kGroupRows ? most_row_tiles(p.M, p.batch, TM) : (p.M + TM - 1) / TM;
-  const int64_t NT = (p.N + cols - 1) / cols;
-  const int64_t n = (GRP == kGroupRows ? 1 : p.batch) * MT * NT;
+// Workgroups of a product in tiles of TM x TN, NT tiles across D; negative: too many.
+template <int GRP, int TM>
+int64_t tile_grid(const TileArgs& p, int64_t MT, int64_t NT) {
   const int64_t splits = p.splits > 1 ? p.splits : 1;
-  if (n == 0) return hipSuccess;
-  if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37)
-    return hipErrorInvalidConfiguration;
-  auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, GRP, TM, TN>;
+  const int64_t n = (GRP == kGroupRows ? 1 : p.batch) * MT * NT;
+  if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37) return -1;
   int64_t grid = n * splits;
-  if (GRP == kGroupRows && TM == 256 && splits == 1) grid += kCus / 2;   // (tiles in halves)
+  if (grid > 0 && GRP == kGroupRows && TM == 256 && splits == 1) grid += kCus / 2;   // (tiles in halves)
   if (GRP == kGroupSums) {   // one for each that the chip holds at once, an equal number a XCD
     constexpr int64_t kPlaces = kCus * (TM == 128 ? 2 : 1);
     grid = (grid + kXcds - 1) / kXcds * kXcds;
     grid = grid < kPlaces ? grid : kPlaces;
   }
-  if (grid > 0x7fffffff) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kTileWaves * kWave), 0, s, p, uint32_t(n),
-                     uint32_t(MT), uint32_t(NT));
+  return grid > 0x7fffffff ? -1 : grid;
+}
+
+template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>
+hipError_t launch_tile_of(const TileArgs& p, hipStream_t s) {
+  const int64_t cols = EPI == kGated ? TN / 2 : TN;
+  const int64_t MT = GRP == kGroupRows ? most_row_tiles(p.M, p.batch, TM) : (p.M + TM - 1) / TM;
+  const int64_t NT = (p.N + cols - 1) / cols;
+  const int64_t grid = tile_grid<GRP, TM>(p, MT, NT);
+  if (grid == 0) return hipSuccess;
+  if (grid < 0) return hipErrorInvalidConfiguration;
+  auto kern = ffn_tile_kernel<DT, SRCA, SRCB, EPI, GRP, TM, TN>;
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(kTileWaves * kWave), 0, s, p,
+                     uint32_t(p.batch * MT * NT), uint32_t(MT), uint32_t(NT));
   return hipGetLastError();
 }
 

@@ -199,6 +199,11 @@ hipError_t launch_grouped_dx(const TileArgs& a, int dtype, hipStream_t s) {
                         : ffn::product<kF16, ffn::kRows, ffn::kPackedT2, ffn::kGroupRows>(a, s);
 }
 
+hipError_t launch_grouped_both(const TileArgs& dx, const TileArgs& dw, int dtype, hipStream_t s) {
+  return dtype == kBF16 ? ffn::both_gradients<kBF16>(dx, dw, s)
+                        : ffn::both_gradients<kF16>(dx, dw, s);
+}
+
 hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s) {
   return dtype == kBF16 ? ffn::product<kBF16, ffn::kTrans, ffn::kTrans, ffn::kGroupSums>(a, s)
                         : ffn::product<kF16, ffn::kTrans, ffn::kTrans, ffn::kGroupSums>(a, s);
