@@ -20,6 +20,8 @@ struct GradPlan {
   bmm::TilePlan dx, dw;
 };
 
+constexpr double kLaunchNs = 4000;
+
 GradPlan plan_grads(const bmm_grouped_desc& d, bool gated) {
   GradPlan p;
   p.sum = d.N;
@@ -30,9 +32,13 @@ GradPlan plan_grads(const bmm_grouped_desc& d, bool gated) {
     p.slopes_bytes = (p.dgu_bytes + (peaks > 0 ? 4 * (1 + peaks) : 0) + 255) / 256 * 256;
   }
   p.dx = bmm::plan_group_rows(d.groups, d.T, d.K, (p.sum + 31) / 32, true);
-  // (slabs of the mean group)
-  p.dw = bmm::plan_tiles(d.groups, p.sum, d.K, (d.T + 32 * d.groups - 1) / (32 * d.groups), true);
-  p.both = p.dx.tile == bmm::kTile128 && p.dw.tile == bmm::kTile128;
+  p.dw = bmm::plan_group_sums(d.groups, d.T, p.sum, d.K, false);
+  if (p.dx.tile == bmm::kTile128) {
+    // one launch, if dW's tiles do not cost more than it saves
+    const bmm::TilePlan small = bmm::plan_group_sums(d.groups, d.T, p.sum, d.K, true);
+    p.both = small.ns <= p.dw.ns + kLaunchNs;
+    if (p.both) p.dw = small;
+  }
   const int64_t dx = p.dx.splits > 1 ? p.dx.splits * d.T * d.K * 4 : 0;
   const int64_t dw = p.dw.splits > 1 ? p.dw.splits * d.groups * p.sum * d.K * 4 : 0;
   p.dw_parts = p.slopes_bytes + (p.both ? (dx + 255) / 256 * 256 : 0);

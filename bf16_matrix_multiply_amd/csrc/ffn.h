@@ -112,6 +112,8 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
 int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs);
 // By E groups of T rows.
 TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool may_split);
+// (small: by tiles of 128 x 128)
+TilePlan plan_group_sums(int64_t E, int64_t T, int64_t M, int64_t N, bool small);
 int plan_group_forward(int64_t E, int64_t T, int64_t N, int64_t slabs);
 
 // ---- activations ----

@@ -230,8 +230,10 @@ hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s) {
 namespace {
 
 // row_tiles(tm): tiles of tm rows; outputs: values that a split sum is held in.
+// The first so many sizes. `extra`: nanoseconds of a tile of each size besides those of its slabs that are added.
 template <class Fn>
-TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool may_split) {
+TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool may_split,
+                 const double (&extra)[4], int sizes = 4) {
   struct Size {
     int64_t tm, tn, places;
     double slab, besides, first, later;
@@ -242,12 +244,12 @@ TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool ma
                                     {256, 256, 256, 672, 9300, .77, .56}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   TilePlan best{kTile128, 1, 0};
-  for (int size = 0; size < 4; ++size) {
+  for (int size = 0; size < sizes; ++size) {
     const Size& z = kSizes[size];
     const double tiles = row_tiles(z.tm) * ((N + z.tn - 1) / z.tn);
     for (int splits : kSplits) {
       if (splits > 1 && (!may_split || slabs / splits < 8)) break;
-      const double tile = double((slabs + splits - 1) / splits) * z.slab + z.besides;
+      const double tile = double((slabs + splits - 1) / splits) * z.slab + z.besides + extra[size];
       const double fill = tiles * splits / z.places, rounds = fill < 1e12 ? double(int64_t(fill)) : fill;
       const double a = rounds > 0 ? z.later : z.first;
       double cost = rounds * tile;
@@ -259,11 +261,13 @@ TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool ma
   return best;
 }
 
+constexpr double kNoExtra[4] = {0, 0, 0, 0};
+
 }  // namespace
 
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
   auto row_tiles = [&](int64_t tm) { return double(batch) * ((M + tm - 1) / tm); };
-  return plan_of(row_tiles, N, slabs, double(batch) * M * N, may_split);
+  return plan_of(row_tiles, N, slabs, double(batch) * M * N, may_split, kNoExtra);
 }
 
 // The host knows T rows and E groups, not how the rows fall on them: groups that have
@@ -274,7 +278,18 @@ TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool ma
     const double tiles = n / tm + (E > 1 ? 0.5 : 0);
     return some * (tiles > 1 ? tiles : 1);
   };
-  return plan_of(row_tiles, N, slabs, double(T) * N, may_split);
+  return plan_of(row_tiles, N, slabs, double(T) * N, may_split, kNoExtra);
+}
+
+// Sums over the rows of E groups of T. Their many results make the difference between the
+// sizes: 24576 rows of 64 groups, 2048 x 1408, by tiles of 128 x 128, 256 x 128, 256 x 192
+// and 256 x 256: 252, 251, 232 and 211 us; 16384 rows of 16 groups, 8192 x 2048: 694, 643,
+// 559 and 529 us.
+TilePlan plan_group_sums(int64_t E, int64_t T, int64_t M, int64_t N, bool small) {
+  static constexpr double kExtra[4] = {2300, 1100, 500, 700};
+  auto row_tiles = [&](int64_t tm) { return double(E) * ((M + tm - 1) / tm); };
+  const int64_t slabs = E > 0 ? (T + 32 * E - 1) / (32 * E) : 0;   // of the mean group
+  return plan_of(row_tiles, N, slabs, double(E) * M * N, true, kExtra, small ? 1 : 4);
 }
 
 // Few rows: the weights are read once for up to 64 rows. Few-rows kernel / 128 x 128
