@@ -52,9 +52,9 @@ __device__ __forceinline__ int small_tiles(int n) {
 }
 
 // A group, the same in every lane: its index, its first row and its rows, and the
-// first row of a tile within the group.
+// number of a tile within the group.
 struct Group {
-  int e, start, rows, at;
+  int e, start, rows, tile;
 };
 
 struct Groups {
@@ -164,27 +164,35 @@ struct Groups {
     }
     return t;
   }
-  // The group of row tile r < total.
+  // The group of row tile r, with its number among the group's; of the full ones, of the
+  // small ones, or of both in the groups' order, the small one last.
   template <int TM>
   __device__ __forceinline__ Group find(const Tiles<TM>& t, int r) const {
-    if (r >= t.grouped) return {E, t.end_all, T - t.end_all, (r - t.grouped) * TM};
-    return search(r, t.first, t.own, [](int n) { return full_tiles<TM>(n); }, TM);
+    if (r >= t.grouped) return behind(t, r - t.grouped);
+    return search(r, t.first, t.own, [](int n) { return full_tiles<TM>(n); });
   }
-  // The group of small row tile r < total_small.
   template <int TM>
   __device__ __forceinline__ Group find_small(const Tiles<TM>& t, int r) const {
-    Group g = {E, t.end_all, T - t.end_all, 0};
-    if (r < t.grouped_small)
-      g = search(r, t.first_small, t.own_small, [](int n) { return small_tiles<TM>(n); }, 0);
-    g.at = g.rows / 256 * 256;
-    return g;
+    if (r >= t.grouped_small) return behind(t, 0);
+    return search(r, t.first_small, t.own_small, [](int n) { return small_tiles<TM>(n); });
+  }
+  template <int TM>
+  __device__ __forceinline__ Group find_any(const Tiles<TM>& t, int r) const {
+    const int grouped = t.grouped + t.grouped_small;
+    if (r >= grouped) return behind(t, r - grouped);
+    return search(r, t.first + t.first_small, t.own + t.own_small,
+                  [](int n) { return full_tiles<TM>(n) + small_tiles<TM>(n); });
   }
 
  private:
+  template <int TM>
+  __device__ __forceinline__ Group behind(const Tiles<TM>& t, int tile) const {
+    return {E, t.end_all, T - t.end_all, tile};
+  }
   // The group of item r, of which each group has items(rows) and this lane's `own` from
-  // `first` on; at: the item's number in the group times `step`.
+  // `first` on, and the item's number in the group.
   template <class Fn>
-  __device__ __forceinline__ Group search(int r, int first, int own, Fn items, int step) const {
+  __device__ __forceinline__ Group search(int r, int first, int own, Fn items) const {
     int e = 0, start = 0, rows = 0, item = 0, left = r - first;
     each([&](int i, int s, int n) {
       const int k = items(n);
@@ -198,7 +206,7 @@ struct Groups {
     });
     const int l = __builtin_ctzll(__builtin_amdgcn_ballot_w64(r >= first && r < first + own));
     return {__builtin_amdgcn_readlane(e, l), __builtin_amdgcn_readlane(start, l),
-            __builtin_amdgcn_readlane(rows, l), __builtin_amdgcn_readlane(item, l) * step};
+            __builtin_amdgcn_readlane(rows, l), __builtin_amdgcn_readlane(item, l)};
   }
 };
 

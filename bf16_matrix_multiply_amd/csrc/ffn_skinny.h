@@ -91,7 +91,7 @@ __global__ __launch_bounds__(W* kWave) void ffn_skinny_kernel(TileArgs p) {
     const Group at = groups.find<16 * MR>(tiles, int(blockIdx.y));
     empty = at.e == int(p.batch);   // the rows behind the last group: an empty sum
     batch = empty ? 0 : at.e;
-    m0 = at.at;
+    m0 = at.tile * (16 * MR);
     d_row = at.start;
     a_off = at.start * p.lda;
     p.M = at.rows;

@@ -486,10 +486,32 @@ __device__ __forceinline__ void slabs_of(Place<GRP>& at, int values, uint32_t sp
 
 constexpr uint32_t kCus = 256;
 
+// Tile v of the k x NT tiles of one group, whose rows are taken in bands of 6 at most
+// and as equal as can be, so that the tiles of a band that run together share the
+// group's weight: its row and column.
+struct BandTile {
+  uint32_t row, col;
+};
+__device__ __forceinline__ BandTile band_tile(uint32_t v, uint32_t k, uint32_t NT) {
+  const uint32_t bands = (k + 5) / 6, low = k / bands, more = k % bands;
+  uint32_t rows = low + 1, row = 0;
+  if (v >= more * rows * NT) {
+    v -= more * rows * NT;
+    row = more * rows;
+    rows = low;
+  }
+  const uint32_t band = v / (rows * NT);
+  v -= band * (rows * NT);
+  const uint32_t col = v / rows;
+  return {row + band * rows + v - col * rows, col};
+}
+
 // Which tile of a product by groups of rows workgroup w makes; false: none. The host
-// knows a bound of the tiles only. Where the full tiles would leave the chip at most
-// half full in their last round, and the small ones find room beside them, those of
-// the last round are made in two halves of 128 rows.
+// knows a bound of the tiles only. `small`: by the body for 128 rows, where a tile of 256
+// holds no more of its group. Where the small tiles are few, they come last, and if the
+// full ones would leave the chip at most half full in their last round and the small
+// ones find room beside them, those of the last round are made in two halves. Where
+// they are many, they stay beside their group's full ones, whose weight they share.
 template <int TM, int COLS>
 __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint32_t NT, int values,
                                             int lane, Place<kGroupRows>& at, bool& small) {
@@ -497,40 +519,49 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint3
   groups.init(p.ends, int(p.batch), int(p.M), lane);
   const auto rows = groups.tiles<TM>(p.zero_tail);
   const uint32_t splits = p.splits > 1 ? p.splits : 1;
-  const uint32_t n_full = rows.total * NT * splits, n_small = rows.total_small * NT * splits;
-  uint32_t cut = 0;   // tiles made in halves
-  if (TM == 256 && splits == 1) {
-    const uint32_t last = n_full % kCus;
-    if (last <= kCus / 2 && 2 * last + n_small <= kCus) cut = last;
+  uint32_t full = rows.total, last = rows.total_small;   // row tiles
+  const bool mixed = TM == 256 && 4 * last >= full;
+  if (mixed) {
+    full += last;
+    last = 0;
   }
-  uint32_t MT = rows.total, half = 0;
-  small = w >= n_full - cut;   // the body for 128 rows
-  bool last = false;           // a small tile
-  if (w < n_full - cut) {
-    w = xcd_run(w, n_full - cut);
-  } else if (w < n_full - cut + n_small) {
-    w = xcd_run(w - (n_full - cut), n_small);
-    MT = rows.total_small;
-    last = true;
-  } else {
-    w -= n_full - cut + n_small;
+  const uint32_t n_full = full * NT * splits, n_last = last * NT * splits;
+  uint32_t cut = 0;   // tiles made in halves
+  if (TM == 256 && splits == 1 && !mixed) {
+    const uint32_t over = n_full % kCus;
+    if (over <= kCus / 2 && 2 * over + n_last <= kCus) cut = over;
+  }
+  uint32_t MT = full, half = 0;
+  const bool halves = w >= n_full - cut + n_last, lasts = !halves && w >= n_full - cut;
+  if (halves) {
+    w -= n_full - cut + n_last;
     if (w >= 2 * cut) return false;
     half = w % 2;
     w = n_full - cut + w / 2;
+  } else if (lasts) {
+    w = xcd_run(w - (n_full - cut), n_last);
+    MT = last;
+  } else {
+    w = xcd_run(w, n_full - cut);
   }
   at.split = w / (MT * NT);
-  const TileAt t = tile_at(w - at.split * (MT * NT), MT, NT, false);
-  const Group g = last ? groups.find_small<TM>(rows, int(t.mt)) : groups.find<TM>(rows, int(t.mt));
+  w -= at.split * (MT * NT);
+  const int r = int(w / NT);
+  const Group g = lasts ? groups.find_small<TM>(rows, r)
+                        : mixed ? groups.find_any<TM>(rows, r) : groups.find<TM>(rows, r);
+  const int k = lasts ? 1 : full_tiles<TM>(g.rows) + (mixed ? small_tiles<TM>(g.rows) : 0);
+  const BandTile t = band_tile(w - uint32_t(r - g.tile) * NT, uint32_t(k), NT);
   at.empty = g.e == int(p.batch);
   at.b = at.empty ? 0 : g.e;
-  at.m0 = g.at + int(128 * half);
-  at.n0 = int(t.nt * COLS);
+  at.m0 = lasts ? g.rows / 256 * 256 : int(t.row * TM + 128 * half);
+  at.n0 = int(t.col * COLS);
   at.M = g.rows;
   at.K = at.empty ? 0 : int(p.K);
   at.d_row = g.start;
   at.a_off = g.start * p.lda;
   at.b_off = at.b * p.b_bs;
   slabs_of(at, values, splits);
+  small = TM == 256 && (halves || at.M - at.m0 <= 128);
   return at.m0 < at.M;
 }
 
