@@ -292,13 +292,23 @@ hipError_t launch_skinny(const TileArgs& p, hipStream_t s) {
   return launch_skinny_of<DT, EPI, kWhole, 4, kWide, 8>(p, s);
 }
 
-// By groups: blocks of 16 rows, or of 32 or 64 where the groups that have rows have
-// more in the mean (the host does not know the groups, only T and E).
+// By groups: blocks of 16 rows, or of 64 where the groups that have rows have more than
+// 16 in the mean (the host does not know the groups, only T and E); but of 16 as long as
+// that gives a chip that would stay half empty more workgroups. 16 / 64 (us, launches from
+// a graph, weights cold):
+//   rows a group                      6          12         20         32         48
+//   4 x 4096 -> 1024, 128 wide        11.6/15.1  12.8/15.5  12.0/20.1  19.3/23.8  20.2/23.0
+//   4 gated the same, 256             14.0/18.3  13.8/19.0  19.3/22.3  27.2/24.0  33.3/24.1
+//   16 x 2048 -> 1024, 512            14.6/15.6  17.0/18.7  21.2/18.9  24.6/25.2  32.3/28.8
+//   8 x 8192 -> 4096, 1024            91.5/102   115/106    163/120    230/149    302/186
+// ("wide": workgroups of one block of rows a group). Blocks of 32 were never the best by
+// more than 4%.
 template <int DT, int EPI>
 hipError_t launch_skinny_groups(const TileArgs& p, hipStream_t s) {
   const int64_t groups = p.batch < p.M ? p.batch : p.M, mean = groups > 0 ? p.M / groups : 0;
-  if (mean <= 8) return launch_skinny_of<DT, EPI, kGroupRows, 1, 2, 8>(p, s);
-  if (mean <= 24) return launch_skinny_of<DT, EPI, kGroupRows, 2, 2, 8>(p, s);
+  const int64_t wide = groups * ((p.N + (EPI == kGated ? 15 : 31)) / (EPI == kGated ? 16 : 32));
+  if (mean <= 16 || (mean <= 48 && wide <= 128))
+    return launch_skinny_of<DT, EPI, kGroupRows, 1, 2, 8>(p, s);
   return launch_skinny_of<DT, EPI, kGroupRows, 4, 2, 8>(p, s);
 }
 

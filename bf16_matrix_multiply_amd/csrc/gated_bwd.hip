@@ -309,9 +309,26 @@ int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs) {
   return plan_tiles(batch, M, N, slabs, false).tile;
 }
 
+// By groups: up to which rows a group (in the mean) the few-rows kernel is the faster
+// one goes by how much of the chip tiles of 128 x 128 would fill. Few-rows kernel, the
+// better of its two blocks / the best tiles (us, launches from a graph, weights cold):
+//   rows a group                      6           12          20          48          96
+//   32 tiles: 4 x 4096 -> 1024        11.6/38.6   12.8/38.8   12.0/39.0   20.2/39.2   25.8/39.5
+//   64 tiles: 4 gated the same        14.0/39.3   13.8/39.8   19.3/39.8   24.1/39.9   44.7/40.5
+//   128 tiles: 16 x 2048 -> 1024      14.6/22.6   17.0/22.9   18.9/23.0   28.8/24.1   43.9/25.0
+//   256 tiles: 8 x 8192 -> 4096       91.5/110    106/113     119/117     186/123     327/149
+//   512 tiles: 8 x 4096 -> 8192       87.0/93.4   101/92.3    113/93.3    172/97.5    325/123
+//   1024 tiles: 64 x 1408 -> 2048     62.4/66.3   80.2/67.9   91.7/69.9   131/78.1    219/89.1
+// and with 8-bit operands alike (8 x 4096 -> 8192: 43.2/48.6, 52.8/47.9, 56.1/48.9). The
+// groups there differ by half in size; more alike ones suit the few-rows kernel (64 rows
+// and a tail of 16 of 8 groups gated 4096 -> 8192: 156 us in its blocks of 16, 208 in
+// tiles), so that up to 10 rows are its own everywhere.
 int plan_group_forward(int64_t E, int64_t T, int64_t N, int64_t slabs) {
-  const int64_t some = E < T ? E : T;
-  if (some > 0 && T / some <= 48 && T / 16 + some < 65535) return kSkinny;
+  const int64_t some = E < T ? E : T, tiles = some * ((N + 127) / 128);
+  if (tiles > 0) {
+    const int64_t rows = 4096 / tiles, limit = rows < 10 ? 10 : rows > 96 ? 96 : rows;
+    if (T / some <= limit && T / 16 + some < 65535) return kSkinny;
+  }
   return plan_group_rows(E, T, N, slabs, false).tile;
 }
 

@@ -29,7 +29,9 @@ SHAPES = [  # (rows of each group, rows behind the last, N, K, columns beside X)
     ([0] * 63 + [9] + [0] * 63 + [2], 5, 56, 64, 0),
     ([127, 128, 129, 0, 256, 1], 30, 136, 144, 40),      # at the tiles' edges
     ([255, 257, 300], 0, 200, 64, 0),
-    ([40, 0, 30, 64, 33], 3, 104, 160, 8),               # few rows in blocks of 64
+    ([40, 0, 30, 64, 33], 3, 104, 160, 8),
+    ([60, 0, 64, 129, 2], 3, 104, 160, 0),               # few rows in blocks of 64
+    (spread(20, 20, 33), 1, 264, 144, 0),
     ([1000, 3, 0, 40], 77, 520, 336, 0),                 # one group much larger
     ([300, 500, 2, 600], 0, 1160, 528, 0),
     ([700, 0, 690], 130, 2056, 48, 8),

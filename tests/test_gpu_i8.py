@@ -181,7 +181,8 @@ def test_gated(i, dtype):
 
 GROUPS = [  # (rows of each group, rows behind the last, N, K)
     ([1], 0, 8, 32), ([0, 1, 0], 2, 136, 512), ([3, 0, 17, 1, 0], 0, 72, 96), ([16, 15, 17], 5, 64, 32),
-    ([1] * 70, 1, 40, 96), ([5, 0, 33, 64, 1], 0, 264, 288), ([40, 0, 30, 64, 33], 3, 104, 160), ([127, 128, 129, 0, 256, 1], 30, 136, 160),
+    ([1] * 70, 1, 40, 96), ([5, 0, 33, 64, 1], 0, 264, 288), ([40, 0, 30, 64, 33], 3, 104, 160), ([60, 0, 64, 129, 2], 3, 104, 160),
+    ([21, 18, 0, 25] * 5, 1, 264, 160), ([127, 128, 129, 0, 256, 1], 30, 136, 160),
     ([1000, 3, 0, 40], 77, 520, 352), ([300, 500, 2, 600], 0, 1160, 544),
 ]
 GROUP_IDS = [f"{len(s[0])}x{sum(s[0])}+{s[1]}_{s[2]}x{s[3]}" for s in GROUPS]

@@ -40,14 +40,16 @@ def test_backward(product, shapes):
 
 
 def test_few_rows_blocks_and_one_launch():
-    """Blocks of 16, 32 and 64 rows; both gradients in one launch, dX split and unsplit."""
-    means = set()
-    for counts, tail, N, K, _ in small.SHAPES:
-        T, E = sum(counts) + tail, len(counts)
-        if T and bmm.group_plan("grouped_mma", E, T, N, K)[0] == "few_rows":
-            mean = T // min(E, T)
-            means.add(16 if mean <= 8 else 32 if mean <= 24 else 64)
-    assert means == {16, 32, 64}
+    """Blocks of 16 and 64 rows; both gradients in one launch, dX split and unsplit."""
+    for kind in ("mma", "gated"):
+        blocks = set()
+        for counts, tail, N, K, _ in small.SHAPES:
+            T, E = sum(counts) + tail, len(counts)
+            if T and bmm.group_plan(f"grouped_{kind}", E, T, N, K)[0] == "few_rows":
+                some = min(E, T)
+                wide = some * -(-N // (16 if kind == "gated" else 32))
+                blocks.add(16 if T // some <= 16 or (T // some <= 48 and wide <= 128) else 64)
+        assert blocks == {16, 64}, kind
     both = set()
     for E, T, N, K in tiles.MMA_BACK + tiles.GATED_BACK:
         for kind in ("mma", "gated"):
