@@ -62,6 +62,7 @@ struct Groups {
   int E, T, per;       // groups, rows, groups a lane
   int lane, before;    // where this lane's first group starts
   int rank;            // this lane's group in the order of size (sort)
+  int filled;          // groups that have rows (sort)
   int end0;            // and its end as read (kept: with 64 groups or fewer nothing is read again)
 
   __device__ __forceinline__ int end(int i, int from) const {   // this lane's i-th group
@@ -109,11 +110,16 @@ struct Groups {
     return {e, __builtin_amdgcn_readlane(start, l), __builtin_amdgcn_readlane(rows, l), 0};
   }
 
-  // Orders the groups by size, the largest first (up to 64 groups; more stay in their
-  // order): rank is the place of this lane's group.
+  // Orders the groups: up to 64 by size, the largest first, and rank is the place of
+  // this lane's group; more as they are, but those without rows last, and rank is the
+  // place of the first of this lane's that has rows.
   __device__ __forceinline__ void sort() {
-    rank = lane;
-    if (per > 1) return;
+    if (per > 1) {
+      const int own = lane_filled(), sum = lanes_sum(own);
+      rank = sum - own;
+      filled = __builtin_amdgcn_readlane(sum, kWave - 1);
+      return;
+    }
     int rows = -1;
     each([&](int, int, int n) { rows = n; });
     int before_it = 0;
@@ -122,10 +128,17 @@ struct Groups {
       before_it += n > rows || (n == rows && j < lane);
     }
     rank = lane < E ? before_it : kWave;
+    filled = __builtin_popcountll(__builtin_amdgcn_ballot_w64(rows > 0));
   }
   // The slot-th group in that order.
   __device__ __forceinline__ Group sorted(int slot) const {
-    if (per > 1) return at(slot);
+    if (per > 1) {
+      const int own = lane_filled();
+      if (slot < filled) return search(slot, rank, own, [](int n) { return int(n > 0); });
+      const int first = lane * per < E ? lane * per : E, left = E - first;
+      return search(slot - filled, first - rank, (left < per ? left : per) - own,
+                    [](int n) { return int(n == 0); });
+    }
     return at(__builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == slot)));
   }
 
@@ -185,6 +198,12 @@ struct Groups {
   }
 
  private:
+  // This lane's groups that have rows.
+  __device__ __forceinline__ int lane_filled() const {
+    int own = 0;
+    each([&](int, int, int n) { own += n > 0; });
+    return own;
+  }
   template <int TM>
   __device__ __forceinline__ Group behind(const Tiles<TM>& t, int tile) const {
     return {E, t.end_all, T - t.end_all, tile};

@@ -73,9 +73,10 @@ void grads_kernel(TileArgs dx, TileArgs dw, uint32_t n_dx, uint32_t NT_dx, uint3
   } else {
     Place<kGroupSums> at;
     list.init(dw, blockIdx.x - n_dx, n_dw, MT_dw, NT_dw, lane);
-    if (!list.template locate<kSide, kSide>(dw, 0, 32, at)) return;
-    make_tile<DT, kTrans, kTrans, kStore, kGroupSums, kSide, kSide, 1>(dw, at, list, ring, lane,
-                                                                      wave);
+    if (list.template locate<kSide, kSide>(dw, 0, 32, at))
+      make_tile<DT, kTrans, kTrans, kStore, kGroupSums, kSide, kSide, 1>(dw, at, list, ring, lane,
+                                                                        wave);
+    fill_empty<1>(list);
   }
 }
 

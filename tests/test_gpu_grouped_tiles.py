@@ -230,3 +230,50 @@ def test_layouts(counts, n, K):
     same(out[:-7], want[:-7], "Y")
     assert torch.isnan(out[-7:]).all()
     same(bmm.grouped_mma(x, ref.pack(w), ends), want, "Y, fresh")
+
+
+# ---- sums of groups without rows ----
+
+def some(E, filled, T):
+    """T rows in `filled` of E groups, the last and the first without rows where they can be."""
+    rng = random.Random(E + filled)
+    chosen = rng.sample(range(1, E - 1), filled) if filled < E - 1 else range(filled)
+    counts = [0] * E
+    for e in [*chosen, *rng.choices(chosen, k=T - filled)][:T]:
+        counts[e] += 1
+    return counts
+
+
+# (groups, those with rows, rows, N, K): a group's sums are less than, exactly and more than
+# the 64 KB that are filled at a time
+EMPTY = [(3, 1, 5, 128, 256), (64, 3, 40, 40, 48), (64, 63, 700, 40, 48), (65, 2, 2, 264, 272),
+         (130, 40, 300, 264, 272), (130, 130, 300, 40, 48), (200, 199, 600, 24, 32),
+         (9, 2, 4000, 264, 272), (1000, 5, 30, 264, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("shape", EMPTY, ids=str)
+def test_empty_groups(shape, dtype):
+    E, filled, T, N, K = shape
+    counts = some(E, filled, T)
+    gen, ends = gen_of(E + T), gref.ends_of(counts).cuda()
+    x, dy = whole(gen, 2, T, K, dtype=dtype), whole(gen, 2, T, N, dtype=dtype)
+    g, u = whole(gen, 1, T, N, dtype=dtype), whole(gen, 1, T, N, dtype=dtype)
+    w = bmm.pack_operand(whole(gen, 2, E, N, K, dtype=dtype), 8)
+    want, want_g, want_u = (torch.zeros(E, N, K, device="cuda") for _ in range(3))
+    on = (g > 0).float()   # relu: dG = dH U there, dU = dH G
+    for e, r in gref.groups(counts):
+        xt = x[r].float().t().contiguous().t()
+        want[e] = dy[r].float().t() @ xt
+        want_g[e] = (dy[r].float() * u[r].float() * on[r]).t() @ xt
+        want_u[e] = (dy[r].float() * g[r].float() * on[r]).t() @ xt
+    for _ in range(2):   # (what an allocation held before)
+        dirt = [torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda") for _ in range(3)]
+        del dirt
+        dw = bmm.grouped_mma_backward(dy, x, w, ends, need_dx=False)[1]
+        same(dw, want, "dW")
+        dirt = [torch.full((E, N, K), float("nan"), dtype=dtype, device="cuda") for _ in range(3)]
+        del dirt, dw
+        _, dwg, dwu = bmm.grouped_gated_backward(dy, g, u, x, w, w, ends, act="relu", need_dx=False)
+        same(dwg, want_g, "dWg")
+        same(dwu, want_u, "dWu")
