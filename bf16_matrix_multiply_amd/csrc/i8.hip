@@ -104,11 +104,19 @@ template <int ET>
 hipError_t quantize(int8_t* codes, float* scales, const void* src, int64_t rows, int64_t K,
                     int64_t ld, hipStream_t s) {
   auto launch = [&](auto kern, int64_t threads) {
-    const int64_t each = threads < 256 ? 256 / threads : 1, blocks = (rows + each - 1) / each;
-    if (blocks > 0x7fffffff) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(kern, dim3(unsigned(blocks)), dim3(unsigned(threads < 256 ? 256 : threads)), 0,
-                       s, codes, scales, src, rows, K, ld);
-    return hipGetLastError();
+    const int64_t each = threads < 256 ? 256 / threads : 1;
+    const int64_t most = each << 21;   // rows of one launch: 2^31 threads (2^32 are refused)
+    for (int64_t first = 0; first < rows; first += most) {
+      const int64_t n = rows - first < most ? rows - first : most;
+      hipLaunchKernelGGL(kern, dim3(unsigned((n + each - 1) / each)),
+                         dim3(unsigned(threads < 256 ? 256 : threads)), 0, s, codes + first * K,
+                         scales + first,
+                         static_cast<const char*>(src) + first * ld * (ET == BMM_ELEM_F32 ? 4 : 2),
+                         n, K, ld);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   };
   if (K <= 64 * 8 * kKept) return launch(quantize_kernel<ET, 64>, 64);
   if (K <= 256 * 8 * kKept) return launch(quantize_kernel<ET, 256>, 256);

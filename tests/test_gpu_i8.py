@@ -247,3 +247,15 @@ def test_one_row_and_every_other_row():
     full = bmm.i8_mma(bmm.I8Operand(a, sa), B)
     assert torch.equal(bmm.i8_mma(bmm.I8Operand(a[4:5], sa[4:5]), B), full[4:5])
     assert torch.equal(bmm.i8_mma(bmm.I8Operand(a[1::2], sa[1::2].contiguous()), B), full[1::2])
+
+
+def test_quantize_rows_of_many_launches():
+    """2^26 + 5 rows: more threads than one launch may have. Row r holds r % 251 + 1."""
+    rows, K = (1 << 26) + 5, 32
+    index = torch.arange(rows, device="cuda", dtype=torch.int32) % 251
+    value = (index + 1).to(torch.bfloat16)
+    codes, scales = bmm.i8_quantize(value[:, None].expand(rows, K).contiguous())
+    assert bool((codes.view(torch.int32) == 0x7f7f7f7f).all())
+    # (divided on the CPU: on the GPU a number as divisor is multiplied by its reciprocal)
+    want = (torch.arange(1, 252, dtype=torch.float32) / torch.tensor(127.0)).cuda()
+    assert torch.equal(scales, want[index])
