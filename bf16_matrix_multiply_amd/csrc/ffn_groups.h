@@ -62,7 +62,7 @@ struct Groups {
   int E, T, per;       // groups, rows, groups a lane
   int lane, before;    // where this lane's first group starts
   int rank;            // this lane's group in the order of size (sort)
-  int filled;          // groups that have rows (sort)
+  int filled, own;     // groups that have rows, and this lane's (sort)
   int end0;            // and its end as read (kept: with 64 groups or fewer nothing is read again)
 
   __device__ __forceinline__ int end(int i, int from) const {   // this lane's i-th group
@@ -114,8 +114,10 @@ struct Groups {
   // this lane's group; more as they are, but those without rows last, and rank is the
   // place of the first of this lane's that has rows.
   __device__ __forceinline__ void sort() {
+    own = 0;
     if (per > 1) {
-      const int own = lane_filled(), sum = lanes_sum(own);
+      each([&](int, int, int n) { own += n > 0; });
+      const int sum = lanes_sum(own);
       rank = sum - own;
       filled = __builtin_amdgcn_readlane(sum, kWave - 1);
       return;
@@ -133,7 +135,6 @@ struct Groups {
   // The slot-th group in that order.
   __device__ __forceinline__ Group sorted(int slot) const {
     if (per > 1) {
-      const int own = lane_filled();
       if (slot < filled) return search(slot, rank, own, [](int n) { return int(n > 0); });
       const int first = lane * per < E ? lane * per : E, left = E - first;
       return search(slot - filled, first - rank, (left < per ? left : per) - own,
@@ -198,12 +199,6 @@ struct Groups {
   }
 
  private:
-  // This lane's groups that have rows.
-  __device__ __forceinline__ int lane_filled() const {
-    int own = 0;
-    each([&](int, int, int n) { own += n > 0; });
-    return own;
-  }
   template <int TM>
   __device__ __forceinline__ Group behind(const Tiles<TM>& t, int tile) const {
     return {E, t.end_all, T - t.end_all, tile};
