@@ -1033,18 +1033,13 @@ __device__ __forceinline__ void make_tile(const TileArgs& p, Place<GRP> at, cons
         later[j] = col + c + 16 < p.N ? (lane & 15) * row_bytes + 4 * (c + 16) : kOutOfRange;
         if (wide) off[j] = col + c < p.N ? (lane & 15) * row_bytes + 4 * c : kOutOfRange;
       }
-      constexpr int kType = any_output(DT) ? kBF16 : DT;
-      const bool f16 = any_output(DT) && p.out_type == BMM_ELEM_F16;
+      static_assert(!any_output(DT), "sums by groups are of 16-bit values");
 #pragma unroll
       for (int i = 0; i < kBM; ++i)
 #pragma unroll
         for (int j = 0; j < kPairsN; ++j) {
-          const f32x4 x = result(i, 2 * j), y = result(i, 2 * j + 1);
-          u32x4 v = join16<kType>(x, y);
-          if constexpr (any_output(DT)) {
-            const u32x4 h = join16<kF16>(x, y);
-            v = f16 ? h : v;
-          }
+          const f32x4 x = result(i, 2 * j);
+          const u32x4 v = join16<DT>(x, result(i, 2 * j + 1));
           store(i, j, wide ? __builtin_bit_cast(u32x4, x) : v, std::integral_constant<int, kAux>{});
         }
       if (wide) {
