@@ -52,7 +52,7 @@ hipError_t join(const TileArgs& a, hipStream_t s) {
 
 // Both gradients of a product by groups in one launch, for products so small that
 // either leaves most of the chip idle: workgroups below n_dx make tiles of dX, the
-// others of dW. (777 rows of 5 groups, 528 -> 1000: 14 and 7 us one after the other.)
+// others of dW. (777 rows of 5 groups, 528 -> 1000 f16: 14.6 us a call, 21.7 with two.)
 template <int DT>
 __global__ __launch_bounds__(kTileWaves* kWave) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void grads_kernel(TileArgs dx, TileArgs dw, uint32_t n_dx, uint32_t NT_dx, uint32_t n_dw,
@@ -80,14 +80,36 @@ void grads_kernel(TileArgs dx, TileArgs dw, uint32_t n_dx, uint32_t NT_dx, uint3
   }
 }
 
+// Workgroups that make dW's tiles beside n_dx that make one of dX each, of n_dw that the
+// chip would hold alone. Those that find no place start when tiles of dX end, and the call
+// then lasts as long as such a tile and their tiles of dW together; fewer, in the places
+// that dX leaves, last as long as the longer of the two. The shorter is taken, by the
+// times of plan_tiles' 128 x 128 tile. As many as the chip holds / in the places left (us):
+// gated block 768 -> 512, 610 rows of 16 groups 24.9 / 20.1; product 1352 -> 128, 216 rows
+// of 41 19.2 / 16.0; and where as many are taken 1024 -> 640, 900 rows of 24 23.0 / 25.0,
+// 3728 -> 120, 105 rows of 95 63 / 83.
+inline int64_t dw_places(const TileArgs& dx, const TileArgs& dw, int64_t n_dx, int64_t n_dw,
+                         int64_t tiles_dw) {
+  constexpr int64_t kPlaces = 2 * kCus;
+  const int64_t left = kPlaces - n_dx;
+  if (left < kXcds || n_dw <= left) return n_dw;
+  auto slabs = [](int64_t n, int64_t parts) { return (n + 32 * parts - 1) / (32 * parts); };
+  const int64_t one_dx = 3600 + 475 * slabs(dx.K, dx.splits);
+  const int64_t one_dw = 5900 + 475 * slabs(dw.K, dw.batch * dw.splits);
+  auto rounds = [&](int64_t places) { return (tiles_dw + places - 1) / places; };
+  const int64_t beside = rounds(left) * one_dw;
+  return (beside > one_dx ? beside : one_dx) < one_dx + rounds(n_dw) * one_dw ? left : n_dw;
+}
+
 template <int DT>
 hipError_t both_gradients(const TileArgs& dx, const TileArgs& dw, hipStream_t s) {
   const int64_t MT = (dw.M + 127) / 128, NT_dx = (dx.N + 127) / 128, NT_dw = (dw.N + 127) / 128;
   int64_t n_dx = tile_grid<kGroupRows, 128>(dx, most_row_tiles(dx.M, dx.batch, 128), NT_dx);
-  const int64_t n_dw = tile_grid<kGroupSums, 128>(dw, MT, NT_dw);
+  int64_t n_dw = tile_grid<kGroupSums, 128>(dw, MT, NT_dw);
   if (n_dx < 0 || n_dw < 0) return hipErrorInvalidConfiguration;
   n_dx = (n_dx + kXcds - 1) / kXcds * kXcds;
   if (n_dx + n_dw > 0x7fffffff) return hipErrorInvalidConfiguration;
+  n_dw = dw_places(dx, dw, n_dx, n_dw, dw.batch * MT * NT_dw * dw.splits);
   if (n_dx + n_dw == 0) return hipSuccess;
   hipLaunchKernelGGL(grads_kernel<DT>, dim3(unsigned(n_dx + n_dw)), dim3(kTileWaves * kWave), 0, s,
                      dx, dw, uint32_t(n_dx), uint32_t(NT_dx), uint32_t(n_dw), uint32_t(MT),

@@ -66,6 +66,18 @@
 // (820 -> 1000-1500 us), workgroups that go on to the next tile, a copy of the loop
 // for each wave with its reads and loads shifted, one barrier for two slabs, and
 // for 4 bits 32 x 32 x 64 MFMAs.
+//
+// By groups: 16384 rows of 8 groups, 8192 -> 4096 bf16, 855-875 us (as many operations as
+// the product of 8192^3; MFMA utilisation 0.66 at 1.5-1.6 GHz); weight gradients of 16384
+// rows of 16 groups, 2048 -> 4096 gated, 535-580 us (0.47 at 2.0 GHz: results of 268 MB
+// from sums of 32 slabs); 24576 rows of 64 groups, 2048 -> 1408 gated with projections kept,
+// f16, 350 us (0.44 at 1.9 GHz: each group's weight comes from memory for the few tiles
+// that share it; with one weight for all of them 296). 8192^3 with 8-bit integers 375-385 us
+// = 2.9 PTOP/s (0.70 at 1.9 GHz).
+// What writes the results faster in a probe, four lanes side by side on 64 bytes of a row,
+// did not pay by groups: with the lanes' results turned in registers for it, the weight
+// gradients of 24576 rows of 64 groups, 2048 x 1408, took 213 us instead of 219, those with
+// fewer rows 2% longer.
 #pragma once
 
 #include <type_traits>

