@@ -69,7 +69,7 @@
 //
 // By groups: 16384 rows of 8 groups, 8192 -> 4096 bf16, 855-875 us (as many operations as
 // the product of 8192^3; MFMA utilisation 0.66 at 1.5-1.6 GHz); weight gradients of 16384
-// rows of 16 groups, 2048 -> 4096 gated, 535-580 us (0.47 at 2.0 GHz: results of 268 MB
+// rows of 16 groups, 2048 -> 4096 gated, 535-580 us (0.47 at 2.0 GHz: results of 537 MB
 // from sums of 32 slabs); 24576 rows of 64 groups, 2048 -> 1408 gated with projections kept,
 // f16, 350 us (0.44 at 1.9 GHz: each group's weight comes from memory for the few tiles
 // that share it; with one weight for all of them 296). 8192^3 with 8-bit integers 375-385 us
