@@ -294,3 +294,58 @@ def test_gradients_side_by_side(shape, dtype):
                    for p in ("dx", "dw"))
     test_mma_backward(shape, dtype)
     test_gated_backward(shape, dtype)
+
+
+# ---- the ends of the ranges ----
+
+# (groups, rows, width, K)
+ENDS = [(4096, 5000, 16, 32), (4096, 1, 8, 16), (2, 3, 8, 1 << 21), (2, 200, 8, 1 << 21),
+        (3, 40, 1 << 20, 32), (2, 300, 1 << 20, 16)]
+
+
+@pytest.mark.parametrize("shape", ENDS, ids=str)
+def test_ends_of_the_ranges(shape):
+    test_mma(shape, BF)
+    test_mma_backward(shape, HF)
+    test_gated(shape, HF)
+    test_gated_backward(shape, BF)
+
+
+def test_ends_of_the_ranges_in_8_bits():
+    test_i8_groups((4096, 5000, 16, 32), BF)
+    test_i8_groups((3, 40, 1 << 20, 32), torch.float32)
+    test_i8((5, 1 << 20, 32), HF)
+    test_i8_gated((200, 1 << 20, 32), BF)
+
+
+@pytest.mark.parametrize("E,T,N,K", [(2, 300, 128, 64), (1, 4100, 2832, 512)])
+def test_widest_rows(E, T, N, K):
+    """Rows 2^21 elements apart, the most there may be: inputs and outputs."""
+    counts, _ = counts_of(E, T, 0)
+    ends, gen, wide = gref.ends_of(counts).cuda(), gen_of(7), 1 << 21
+
+    def spread(t):
+        out = torch.empty(T, wide, dtype=t.dtype, device="cuda")[:, 64:64 + t.shape[1]]
+        return out.copy_(t)
+    x, dy = whole(gen, 2, T, K, dtype=BF), whole(gen, 2, T, N, dtype=BF)
+    w = ref.pack(whole(gen, 2, E, N, K, dtype=BF))
+    far = spread(x)
+    y = bmm.grouped_mma(x, w, ends, out=torch.full((T, N), 9, dtype=BF, device="cuda"))
+    same(bmm.grouped_mma(far, w, ends, out=spread(torch.full((T, N), 9, dtype=BF, device="cuda"))),
+         y.float(), "Y")
+    h = bmm.grouped_gated(x, w, w, ends, act="relu")
+    same(bmm.grouped_gated(far, w, w, ends, act="relu"), h.float(), "H")
+    want = bmm.grouped_mma_backward(dy, x, w, ends)
+    far_y = spread(dy)
+    for a, b in zip(bmm.grouped_mma_backward(far_y, far, w, ends), want):
+        same(a, b.float(), "gradients")
+    want = bmm.grouped_gated_backward(dy, dy, dy, x, w, w, ends, act="relu")
+    for a, b in zip(bmm.grouped_gated_backward(far_y, far_y, far_y, far, w, w, ends, act="relu"), want):
+        same(a, b.float(), "gated gradients")
+    del far, far_y
+    q, s = codes(8, T, K)
+    b, sb = codes(9, E, N, K)
+    far = torch.empty(T, 2 * wide, dtype=torch.int8, device="cuda")[:, 64:64 + K].copy_(q)
+    packed = bmm.i8_pack(bmm.I8Operand(b, sb))
+    d = bmm.i8_mma(bmm.I8Operand(q, s), packed, ends)
+    same(bmm.i8_mma(bmm.I8Operand(far, s), packed, ends), d, "8 bits")
