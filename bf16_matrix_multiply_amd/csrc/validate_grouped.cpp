@@ -77,7 +77,8 @@ Status check_grouped_backward(const GroupedGrads& g, const int32_t* ends, const 
   const int64_t w = d->groups * d->N * d->K * 2;
   if (gated && !g.dW != !g.dW1 && w > 0)
     return failw(what, BMM_EINVAL, "dWg and dWu are given both or neither");
-  if (!g.dX && !g.dW && (w > 0 || d->T * d->K > 0))
+  // (an empty gradient has no address: where either is empty, it may be the wanted one)
+  if (!g.dX && !g.dW && w > 0 && d->T * d->K > 0)
     return failw(what, BMM_EINVAL, "no gradient is wanted");
   if (d->K == 0 || (d->T == 0 && w == 0)) return Status{};
   const int64_t y_bytes = d->N * 2, y_ld = d->ld_y * 2;

@@ -652,7 +652,8 @@ int bmm_grouped_mma(uint16_t* Y, const uint16_t* X, const uint32_t* W, const int
  *
  * dX   (T, K) contiguous, or NULL when it is not wanted.
  * dW   (groups, N, K) contiguous and row-major, or NULL. A group without rows
- *      gets zeros.
+ *      gets zeros. (One that is empty, dX for T = 0 or dW for N = 0, is NULL also
+ *      where it is wanted.)
  * dY   (T, ld_y); X (T, ld_x); W may be NULL when dX is, X when dW is.
  * Sums are float32, rounded once; the result is the same on every run.
  * workspace  device memory of at least bmm_grouped_mma_backward_workspace_bytes
