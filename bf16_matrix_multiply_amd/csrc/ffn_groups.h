@@ -14,6 +14,7 @@
 #include <stdint.h>
 
 #include "common.h"
+#include "group_counts.h"
 
 namespace bmm {
 namespace ffn {
@@ -38,17 +39,6 @@ __device__ __forceinline__ int lanes_sum(int x) {
 // The value of the lane before; lane 0: 0.
 __device__ __forceinline__ int lane_before(int x) {
   return __builtin_amdgcn_update_dpp(0, x, 0x138, 0xf, 0xf, false);   // wave_shr:1
-}
-
-// The tiles that n rows take: of TM rows, the last one perhaps not full; with tiles of
-// 256 rows a last one of at most 128 is a small one, of 128 rows.
-template <int TM>
-__device__ __forceinline__ int full_tiles(int n) {
-  return TM == 256 ? (n + 127) / 256 : (n + TM - 1) / TM;
-}
-template <int TM>
-__device__ __forceinline__ int small_tiles(int n) {
-  return TM == 256 && n % 256 > 0 && n % 256 <= 128;
 }
 
 // A group, the same in every lane: its index, its first row and its rows, and the
@@ -223,12 +213,6 @@ struct Groups {
             __builtin_amdgcn_readlane(rows, l), __builtin_amdgcn_readlane(item, l)};
   }
 };
-
-// The most tiles, small ones among them, that T rows in E groups and a tail can take.
-inline int64_t most_row_tiles(int64_t T, int64_t E, int64_t TM) {
-  const int64_t some = E + 1 < T ? E + 1 : T;
-  return (T + some * (TM - 1)) / TM;
-}
 
 }  // namespace ffn
 }  // namespace bmm

@@ -484,16 +484,9 @@ struct Place {
 // The slabs of split `at.split`.
 template <int GRP>
 __device__ __forceinline__ void slabs_of(Place<GRP>& at, int values, uint32_t splits) {
-  using Int = typename Place<GRP>::Int;
-  const Int slabs = (at.K + values - 1) / values;
-  at.s0 = 0;
-  at.s1 = slabs;
-  if (splits > 1) {
-    // (a split starts at an even slab: rows come two slabs at a time)
-    const uint32_t pairs = uint32_t((slabs + 1) / 2), q = pairs / splits, r = pairs % splits;
-    at.s0 = 2 * (Int(at.split) * q + (at.split < r ? at.split : r));
-    if (at.split + 1 < splits) at.s1 = at.s0 + 2 * (q + (at.split < r ? 1 : 0));
-  }
+  const auto r = slab_range(at.K, values, at.split, splits);
+  at.s0 = r.first;
+  at.s1 = r.end;
 }
 
 constexpr uint32_t kCus = 256;

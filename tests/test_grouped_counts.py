@@ -1,0 +1,108 @@
+"""The counts of the products by groups (csrc/group_counts.h: the arithmetic that the
+kernels use) against Python's whole numbers, up to 2^31 - 1 rows (CPU); and products of
+that many rows on the GPU."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import bf16_matrix_multiply_amd as bmm
+from tests import ffn_ref as ref
+from tests import grouped_ref as gref
+
+BF = torch.bfloat16
+TOP = 2 ** 31 - 1
+CSRC = os.path.join(os.path.dirname(bmm.__file__), "csrc")
+SOURCE = """
+#include "group_counts.h"
+using namespace bmm::ffn;
+extern "C" {
+int full(int tm, int n) {
+  return tm == 16 ? full_tiles<16>(n) : tm == 64 ? full_tiles<64>(n)
+       : tm == 128 ? full_tiles<128>(n) : full_tiles<256>(n);
+}
+int small(int tm, int n) { return tm == 128 ? small_tiles<128>(n) : small_tiles<256>(n); }
+int64_t most(int64_t T, int64_t E, int64_t tm) { return most_row_tiles(T, E, tm); }
+void range32(int K, int values, unsigned split, unsigned splits, int* out) {
+  const auto r = slab_range(int32_t(K), values, split, splits);
+  out[0] = r.first;
+  out[1] = r.end;
+}
+void range64(int64_t K, int values, unsigned split, unsigned splits, int64_t* out) {
+  const auto r = slab_range(K, values, split, splits);
+  out[0] = r.first;
+  out[1] = r.end;
+}
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def counts(tmp_path_factory):
+    here = tmp_path_factory.mktemp("counts")
+    (here / "counts.cpp").write_text(SOURCE)
+    out = str(here / "counts.so")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-fsanitize=undefined",
+                           "-fno-sanitize-recover=undefined", "-static-libubsan", "-shared", "-fPIC",
+                           f"-I{CSRC}", str(here / "counts.cpp"), "-o", out])
+    lib = ctypes.CDLL(out)
+    lib.most.restype = ctypes.c_int64
+    lib.most.argtypes = [ctypes.c_int64] * 3
+    lib.range64.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_uint, ctypes.c_uint, ctypes.c_void_p]
+    return lib
+
+
+ROWS = sorted({n for c in (0, 16, 64, 128, 256, 512, 1 << 20, TOP) for d in range(-300, 301)
+               for n in [c + d] if 0 <= n <= TOP})
+
+
+@pytest.mark.parametrize("tm", [16, 64, 128, 256])
+def test_row_tiles(counts, tm):
+    for n in ROWS:
+        small = int(tm == 256 and 0 < n % 256 <= 128)
+        assert counts.full(tm, n) == -(-n // tm) - small, n
+        if tm >= 128:
+            assert counts.small(tm, n) == small, n
+        for E in (1, 4096):   # all rows in one group, the others empty
+            assert counts.most(n, E, tm) >= -(-n // tm)
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3, 12, 32])
+def test_slabs(counts, splits):
+    """Every slab is in one part, in order; a part starts at an even slab and may end one
+    behind the last, which reads as zeros."""
+    for out, fn in (((ctypes.c_int * 2)(), counts.range32), ((ctypes.c_int64 * 2)(), counts.range64)):
+        for K in ROWS if splits == 1 else ROWS[::3]:
+            slabs, at = -(-K // 32), 0
+            for s in range(splits):
+                fn(K, 32, s, splits, out)
+                first, end = out
+                assert 0 <= first <= slabs + 1 and first % 2 == 0 and end <= slabs + 1, (K, s)
+                if end > first:
+                    assert first == at, (K, s)
+                    at = end
+            assert at in (slabs, slabs + slabs % 2), (K, at)
+
+
+@pytest.mark.gpu
+def test_weight_gradient_of_the_most_rows():
+    """2^31 - 1 rows in one group, and in three; all of them zeros but a few at the ends of
+    the groups and of the sums' parts."""
+    K, N = 16, 8
+    x = torch.zeros(TOP, K, dtype=BF, device="cuda")
+    dy = torch.zeros(TOP, N, dtype=BF, device="cuda")
+    at = torch.tensor([0, 1, 5000, TOP // 2, TOP // 2 + 1, TOP - 300, TOP - 32, TOP - 1], device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x[at] = torch.randint(-2, 3, (len(at), K), generator=gen, device="cuda").to(BF)
+    dy[at] = torch.randint(-2, 3, (len(at), N), generator=gen, device="cuda").to(BF)
+    for rows in ([TOP], [1, TOP - 301, 300], [TOP // 2 + 1, 0, TOP - TOP // 2 - 1]):
+        E = len(rows)
+        w = ref.pack(torch.zeros(E, N, K, dtype=BF, device="cuda"))
+        _, dw = bmm.grouped_mma_backward(dy, x, w, gref.ends_of(rows).cuda(), need_dx=False)
+        for e, r in gref.groups(rows):
+            mine = at[(at >= r.start) & (at < r.stop)]
+            want = dy[mine].double().t().contiguous() @ x[mine].double()
+            assert torch.equal(dw[e].double(), want), (rows, e)
+        assert all((dw[e] == 0).all() for e in range(E) if rows[e] == 0)
