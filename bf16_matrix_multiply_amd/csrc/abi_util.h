@@ -16,7 +16,8 @@ inline int report(const Status& st) {
 
 inline int hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return report(Status{});
-  set_last_error(std::string(what) + ": " + hipGetErrorString(e));
+  set_last_error(std::string(what) + ": " + hipGetErrorString(e) +
+                 (e == hipErrorInvalidConfiguration ? " (more tiles than one launch may have)" : ""));
   return BMM_EHIP;
 }
 

@@ -102,6 +102,9 @@ hipError_t launch_mx4_dequantize(void* dst, const uint8_t* codes, const uint8_t*
 hipError_t launch_mx4_mma(const TileArgs& a, hipStream_t s);
 hipError_t launch_mx4_gated(const TileArgs& a, hipStream_t s);
 
+// HIP takes fewer than 2^32 threads along x: the most workgroups of 256 of a launch.
+constexpr int64_t kMaxWorkgroups = (int64_t(1) << 24) - 1;
+
 // How a product of M rows, N columns (gated: of both weights) and so many slabs is cut.
 struct TilePlan {
   int tile, splits;

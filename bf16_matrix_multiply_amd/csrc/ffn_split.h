@@ -108,7 +108,7 @@ hipError_t both_gradients(const TileArgs& dx, const TileArgs& dw, hipStream_t s)
   int64_t n_dw = tile_grid<kGroupSums, 128>(dw, MT, NT_dw);
   if (n_dx < 0 || n_dw < 0) return hipErrorInvalidConfiguration;
   n_dx = (n_dx + kXcds - 1) / kXcds * kXcds;
-  if (n_dx + n_dw > 0x7fffffff) return hipErrorInvalidConfiguration;
+  if (n_dx + n_dw > kMaxWorkgroups) return hipErrorInvalidConfiguration;
   n_dw = dw_places(dx, dw, n_dx, n_dw, dw.batch * MT * NT_dw * dw.splits);
   if (n_dx + n_dw == 0) return hipSuccess;
   hipLaunchKernelGGL(grads_kernel<DT>, dim3(unsigned(n_dx + n_dw)), dim3(kTileWaves * kWave), 0, s,

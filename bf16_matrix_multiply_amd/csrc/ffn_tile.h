@@ -1165,7 +1165,10 @@ template <int GRP, int TM>
 int64_t tile_grid(const TileArgs& p, int64_t MT, int64_t NT) {
   const int64_t splits = p.splits > 1 ? p.splits : 1;
   const int64_t n = (GRP == kGroupRows ? 1 : p.batch) * MT * NT;
-  if (n * splits > 0x7fffffff || NT > 1 << 28 || p.K >= int64_t(1) << 37) return -1;
+  // (sums: their units are counted in 32 bits)
+  if (n * splits > (GRP == kGroupSums ? 0x7fffffff : kMaxWorkgroups) || NT > 1 << 28 ||
+      p.K >= int64_t(1) << 37)
+    return -1;
   int64_t grid = n * splits;
   if (grid > 0 && GRP == kGroupRows && TM == 256 && splits == 1) grid += kCus / 2;   // (tiles in halves)
   if (GRP == kGroupSums) {   // one for each that the chip holds at once, an equal number a XCD
@@ -1173,7 +1176,7 @@ int64_t tile_grid(const TileArgs& p, int64_t MT, int64_t NT) {
     grid = (grid + kXcds - 1) / kXcds * kXcds;
     grid = grid < kPlaces ? grid : kPlaces;
   }
-  return grid > 0x7fffffff ? -1 : grid;
+  return grid > kMaxWorkgroups ? -1 : grid;
 }
 
 template <int DT, int SRCA, int SRCB, int EPI, int GRP, int TM, int TN>

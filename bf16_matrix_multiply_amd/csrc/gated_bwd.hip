@@ -229,10 +229,11 @@ hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s) {
 // tiles, which write the last columns in pieces of 32 bytes, the slowest (369 there).
 namespace {
 
-// row_tiles(tm): tiles of tm rows; outputs: values that a split sum is held in.
+// row_tiles(tm): tiles of tm rows; most(tm): as many at most; outputs: values that a split
+// sum is held in. A size whose tiles are more than one launch may have is not taken.
 // The first so many sizes. `extra`: nanoseconds of a tile of each size besides those of its slabs that are added.
-template <class Fn>
-TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool may_split,
+template <class Fn, class Most>
+TilePlan plan_of(Fn row_tiles, Most most, int64_t N, int64_t slabs, double outputs, bool may_split,
                  const double (&extra)[4], int sizes = 4) {
   struct Size {
     int64_t tm, tn, places;
@@ -244,18 +245,21 @@ TilePlan plan_of(Fn row_tiles, int64_t N, int64_t slabs, double outputs, bool ma
                                     {256, 256, 256, 672, 9300, .77, .56}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   TilePlan best{kTile128, 1, 0};
+  bool any = false;
   for (int size = 0; size < sizes; ++size) {
     const Size& z = kSizes[size];
-    const double tiles = row_tiles(z.tm) * ((N + z.tn - 1) / z.tn);
+    const double cols = double((N + z.tn - 1) / z.tn), tiles = row_tiles(z.tm) * cols;
     for (int splits : kSplits) {
       if (splits > 1 && (!may_split || slabs / splits < 8)) break;
+      if (most(z.tm) * cols * splits + 128 > kMaxWorkgroups) break;   // (128: tiles in halves)
       const double tile = double((slabs + splits - 1) / splits) * z.slab + z.besides + extra[size];
       const double fill = tiles * splits / z.places, rounds = fill < 1e12 ? double(int64_t(fill)) : fill;
       const double a = rounds > 0 ? z.later : z.first;
       double cost = rounds * tile;
       if (fill > rounds) cost += tile * (a + (1 - a) * (fill - rounds));
       if (splits > 1) cost += 4000 + 8e-3 / 5 * splits * outputs;
-      if ((size == 0 && splits == 1) || cost < best.ns) best = {size, splits, cost};
+      if (!any || cost < best.ns) best = {size, splits, cost};
+      any = true;
     }
   }
   return best;
@@ -267,7 +271,7 @@ constexpr double kNoExtra[4] = {0, 0, 0, 0};
 
 TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may_split) {
   auto row_tiles = [&](int64_t tm) { return double(batch) * ((M + tm - 1) / tm); };
-  return plan_of(row_tiles, N, slabs, double(batch) * M * N, may_split, kNoExtra);
+  return plan_of(row_tiles, row_tiles, N, slabs, double(batch) * M * N, may_split, kNoExtra);
 }
 
 // The host knows T rows and E groups, not how the rows fall on them: groups that have
@@ -278,7 +282,8 @@ TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool ma
     const double tiles = n / tm + (E > 1 ? 0.5 : 0);
     return some * (tiles > 1 ? tiles : 1);
   };
-  return plan_of(row_tiles, N, slabs, double(T) * N, may_split, kNoExtra);
+  auto most = [&](int64_t tm) { return double(ffn::most_row_tiles(T, E, tm)); };
+  return plan_of(row_tiles, most, N, slabs, double(T) * N, may_split, kNoExtra);
 }
 
 // Sums over the rows of E groups of T. Their many results make the difference between the
@@ -289,7 +294,8 @@ TilePlan plan_group_sums(int64_t E, int64_t T, int64_t M, int64_t N, bool small)
   static constexpr double kExtra[4] = {2300, 1100, 500, 700};
   auto row_tiles = [&](int64_t tm) { return double(E) * ((M + tm - 1) / tm); };
   const int64_t slabs = E > 0 ? (T + 32 * E - 1) / (32 * E) : 0;   // of the mean group
-  return plan_of(row_tiles, N, slabs, double(E) * M * N, true, kExtra, small ? 1 : 4);
+  auto most = [](int64_t) { return 0.0; };   // (a workgroup makes as many as there are)
+  return plan_of(row_tiles, most, N, slabs, double(E) * M * N, true, kExtra, small ? 1 : 4);
 }
 
 // Few rows: the weights are read once for up to 64 rows. Few-rows kernel / 128 x 128

@@ -726,6 +726,8 @@ int bmm_i8_quantize(int8_t* codes, float* scales, const void* src, int64_t batch
  *   elem_type  of D: BMM_ELEM_F32, _F16 or _BF16 (gated: _F16 or _BF16)
  *   act        bmm_act of the gated block (0 otherwise)
  *   zero_tail  with ends, as in bmm_grouped_desc
+ * More tiles than one launch may have (2^24 workgroups: without ends, batch * M from
+ * about 2^32 on) are refused with BMM_EHIP.
  */
 typedef struct {
   int64_t batch;

@@ -1,6 +1,6 @@
 """The counts of the products by groups (csrc/group_counts.h: the arithmetic that the
 kernels use) against Python's whole numbers, up to 2^31 - 1 rows (CPU); and products of
-that many rows on the GPU."""
+that many rows on the GPU, which one launch of fewer than 2^32 threads has to hold."""
 import ctypes
 import os
 import subprocess
@@ -11,6 +11,8 @@ import torch
 import bf16_matrix_multiply_amd as bmm
 from tests import ffn_ref as ref
 from tests import grouped_ref as gref
+from tests.test_ffn_refuse import L, P, err  # noqa: F401
+from tests.test_grouped_refuse import i8
 
 BF = torch.bfloat16
 TOP = 2 ** 31 - 1
@@ -86,6 +88,34 @@ def test_slabs(counts, splits):
             assert at in (slabs, slabs + slabs % 2), (K, at)
 
 
+def workgroups(tile, splits, T, N, E=1):
+    tm, tn = map(int, tile.split("x"))
+    return (T + (E + 1) * (tm - 1)) // tm * -(-N // tn) * splits + 128
+
+
+@pytest.mark.parametrize("groups,T", [(1, TOP), (7, TOP), (4096, TOP), (4096, TOP - 600000)])
+@pytest.mark.parametrize("product,N,K", [
+    ("grouped_mma", 8, 16), ("grouped_mma", 48, 32), ("grouped_mma_dx", 8, 16), ("grouped_mma_dx", 64, 48),
+    ("grouped_gated", 8, 16), ("grouped_gated_dx", 8, 16), ("i8_mma", 8, 32), ("i8_gated", 16, 32)])
+def test_most_rows_in_one_launch(product, groups, T, N, K):
+    tile, splits = bmm.group_plan(product, groups, T, N, K)
+    width = K if product.endswith("dx") else 2 * N if "gated" in product else N
+    assert workgroups(tile, splits, T, width, groups) < 1 << 24, tile
+
+
+@pytest.mark.parametrize("M", [(1 << 31) - 128, 1 << 31, (1 << 32) - 40000])
+def test_most_rows_of_one_weight(M):
+    for tile, splits in (bmm.group_plan("i8_mma", 0, min(M, TOP), 8, 32), bmm.ffn_plan("gated", 1, M, 8, 16),
+                         bmm.ffn_plan("mx4_mma", 1, M, 64, 32)):
+        assert tile.startswith("256"), tile
+
+
+def test_more_tiles_than_a_launch_holds(L):  # noqa: F811
+    """Refused on the host, with the reason."""
+    assert i8(L, D=1 << 62, M=1 << 33, N=8, K=32, ld_a=32, ld_d=8) < 0
+    assert "more tiles than one launch may have" in err(L)
+
+
 @pytest.mark.gpu
 def test_weight_gradient_of_the_most_rows():
     """2^31 - 1 rows in one group, and in three; all of them zeros but a few at the ends of
@@ -106,3 +136,29 @@ def test_weight_gradient_of_the_most_rows():
             want = dy[mine].double().t().contiguous() @ x[mine].double()
             assert torch.equal(dw[e].double(), want), (rows, e)
         assert all((dw[e] == 0).all() for e in range(E) if rows[e] == 0)
+
+
+@pytest.mark.gpu
+def test_products_of_the_most_rows():
+    """Forward product and dX of 2^31 - 1 rows, zeros but for a few; every output written."""
+    K, N = 16, 8
+    at = torch.tensor([0, 255, 256, 5000, TOP // 2, TOP - 257, TOP - 256, TOP - 1], device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    rows = [5000, TOP - 5257, 0, 257]
+    ends = gref.ends_of(rows).cuda()
+    w = torch.randint(-2, 3, (4, N, K), generator=gen, device="cuda").to(BF)
+    group = torch.bucketize(at, ends.long(), right=True)
+
+    def only(t, want):
+        """t is `want` in the rows `at` and zero elsewhere."""
+        assert torch.equal(t[at].double(), want)
+        t[at] = 0
+        assert not any(part.any() for part in t.split(1 << 27))
+    x = torch.zeros(TOP, K, dtype=BF, device="cuda")
+    x[at] = torch.randint(-2, 3, (len(at), K), generator=gen, device="cuda").to(BF)
+    y = torch.full((TOP, N), float("nan"), dtype=BF, device="cuda")
+    bmm.grouped_mma(x, ref.pack(w), ends, out=y)
+    only(y, (w[group].double() * x[at].double()[:, None]).sum(2))
+    y[at] = torch.randint(-2, 3, (len(at), N), generator=gen, device="cuda").to(BF)
+    dx, _ = bmm.grouped_mma_backward(y, x, ref.pack(w), ends, need_dw=False)
+    only(dx, (w[group].double() * y[at].double()[:, :, None]).sum(1))
