@@ -489,34 +489,9 @@ __device__ __forceinline__ void slabs_of(Place<GRP>& at, int values, uint32_t sp
   at.s1 = r.end;
 }
 
-constexpr uint32_t kCus = 256;
-
-// Tile v of the k x NT tiles of one group, whose rows are taken in bands of 6 at most
-// and as equal as can be, so that the tiles of a band that run together share the
-// group's weight: its row and column.
-struct BandTile {
-  uint32_t row, col;
-};
-__device__ __forceinline__ BandTile band_tile(uint32_t v, uint32_t k, uint32_t NT) {
-  const uint32_t bands = (k + 5) / 6, low = k / bands, more = k % bands;
-  uint32_t rows = low + 1, row = 0;
-  if (v >= more * rows * NT) {
-    v -= more * rows * NT;
-    row = more * rows;
-    rows = low;
-  }
-  const uint32_t band = v / (rows * NT);
-  v -= band * (rows * NT);
-  const uint32_t col = v / rows;
-  return {row + band * rows + v - col * rows, col};
-}
-
 // Which tile of a product by groups of rows workgroup w makes; false: none. The host
 // knows a bound of the tiles only. `small`: by the body for 128 rows, where a tile of 256
-// holds no more of its group. Where the small tiles are few, they come last, and if the
-// full ones would leave the chip at most half full in their last round and the small
-// ones find room beside them, those of the last round are made in two halves. Where
-// they are many, they stay beside their group's full ones, whose weight they share.
+// holds no more of its group. How they lie: row_layout (group_counts.h).
 template <int TM, int COLS>
 __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint32_t NT, int values,
                                             int lane, Place<kGroupRows>& at, bool& small) {
@@ -524,19 +499,10 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint3
   groups.init(p.ends, int(p.batch), int(p.M), lane);
   const auto rows = groups.tiles<TM>(p.zero_tail);
   const uint32_t splits = p.splits > 1 ? p.splits : 1;
-  uint32_t full = rows.total, last = rows.total_small;   // row tiles
-  const bool mixed = TM == 256 && 4 * last >= full;
-  if (mixed) {
-    full += last;
-    last = 0;
-  }
-  const uint32_t n_full = full * NT * splits, n_last = last * NT * splits;
-  uint32_t cut = 0;   // tiles made in halves
-  if (TM == 256 && splits == 1 && !mixed) {
-    const uint32_t over = n_full % kCus;
-    if (over <= kCus / 2 && 2 * over + n_last <= kCus) cut = over;
-  }
-  uint32_t MT = full, half = 0;
+  const RowLayout lay = row_layout<TM>(rows.total, rows.total_small, NT, splits);
+  const bool mixed = lay.mixed;
+  const uint32_t n_full = lay.full * NT * splits, n_last = lay.last * NT * splits, cut = lay.cut;
+  uint32_t MT = lay.full, half = 0;
   const bool halves = w >= n_full - cut + n_last, lasts = !halves && w >= n_full - cut;
   if (halves) {
     w -= n_full - cut + n_last;
@@ -545,7 +511,7 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint3
     w = n_full - cut + w / 2;
   } else if (lasts) {
     w = xcd_run(w - (n_full - cut), n_last);
-    MT = last;
+    MT = lay.last;
   } else {
     w = xcd_run(w, n_full - cut);
   }

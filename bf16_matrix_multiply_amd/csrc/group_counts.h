@@ -50,5 +50,51 @@ constexpr SlabRange<Int> slab_range(Int K, int values, uint32_t split, uint32_t 
   return r;
 }
 
+constexpr uint32_t kCus = 256;
+
+// How the row tiles of a product by groups lie, `full` ones and `small` ones of 128 rows
+// (tiles of 256 rows only) across NT tiles of columns. Where the small ones are few, they
+// come last, and if the full ones would leave the chip at most half full in their last
+// round and the small ones find room beside them, those of the last round are made in two
+// halves. Where they are many, they stay beside their group's full ones, whose weight
+// they share.
+struct RowLayout {
+  uint32_t full, last;   // row tiles: those of the groups in turn, and small ones after them
+  bool mixed;            // the small ones are among the full ones
+  uint32_t cut;          // tiles made in halves
+};
+template <int TM>
+constexpr RowLayout row_layout(uint32_t full, uint32_t small, uint32_t NT, uint32_t splits) {
+  RowLayout l{full, small, TM == 256 && 4 * small >= full, 0};
+  if (l.mixed) {
+    l.full += small;
+    l.last = 0;
+  }
+  const uint32_t over = l.full * NT * splits % kCus;
+  if (TM == 256 && splits == 1 && !l.mixed && over <= kCus / 2 && 2 * over + l.last * NT <= kCus)
+    l.cut = over;
+  return l;
+}
+
+// Tile v of the k x NT tiles of one group, whose rows are taken in bands of 6 at most
+// and as equal as can be, so that the tiles of a band that run together share the
+// group's weight: its row and column.
+struct BandTile {
+  uint32_t row, col;
+};
+constexpr BandTile band_tile(uint32_t v, uint32_t k, uint32_t NT) {
+  const uint32_t bands = (k + 5) / 6, low = k / bands, more = k % bands;
+  uint32_t rows = low + 1, row = 0;
+  if (v >= more * rows * NT) {
+    v -= more * rows * NT;
+    row = more * rows;
+    rows = low;
+  }
+  const uint32_t band = v / (rows * NT);
+  v -= band * (rows * NT);
+  const uint32_t col = v / rows;
+  return {row + band * rows + v - col * rows, col};
+}
+
 }  // namespace ffn
 }  // namespace bmm

@@ -3,6 +3,7 @@ kernels use) against Python's whole numbers, up to 2^31 - 1 rows (CPU); and prod
 that many rows on the GPU, which one launch of fewer than 2^32 threads has to hold."""
 import ctypes
 import os
+import random
 import subprocess
 
 import pytest
@@ -11,6 +12,8 @@ import torch
 import bf16_matrix_multiply_amd as bmm
 from tests import ffn_ref as ref
 from tests import grouped_ref as gref
+from tests import test_gpu_grouped_tiles as tiles
+from tests import test_grouped_coverage as coverage
 from tests.test_ffn_refuse import L, P, err  # noqa: F401
 from tests.test_grouped_refuse import i8
 
@@ -26,6 +29,18 @@ int full(int tm, int n) {
        : tm == 128 ? full_tiles<128>(n) : full_tiles<256>(n);
 }
 int small(int tm, int n) { return tm == 128 ? small_tiles<128>(n) : small_tiles<256>(n); }
+void layout256(unsigned full, unsigned small, unsigned NT, unsigned splits, unsigned* out) {
+  const auto l = row_layout<256>(full, small, NT, splits);
+  out[0] = l.full;
+  out[1] = l.last;
+  out[2] = l.mixed;
+  out[3] = l.cut;
+}
+void band(unsigned v, unsigned k, unsigned NT, unsigned* out) {
+  const auto t = band_tile(v, k, NT);
+  out[0] = t.row;
+  out[1] = t.col;
+}
 int64_t most(int64_t T, int64_t E, int64_t tm) { return most_row_tiles(T, E, tm); }
 void range32(int K, int values, unsigned split, unsigned splits, int* out) {
   const auto r = slab_range(int32_t(K), values, split, splits);
@@ -86,6 +101,43 @@ def test_slabs(counts, splits):
                     assert first == at, (K, s)
                     at = end
             assert at in (slabs, slabs + slabs % 2), (K, at)
+
+
+def row_layout(counts, groups, NT):
+    """The kernel's layout of these groups' 256-row tiles, as test_grouped_coverage's."""
+    out = (ctypes.c_uint * 4)()
+    full = sum(counts.full(256, n) for n in groups)
+    counts.layout256(full, sum(counts.small(256, n) for n in groups), NT, 1, out)
+    tiles, last, mixed, cut = out
+    some = any(0 < n % 256 <= 128 for n in groups)
+    return bool(mixed) and some, last > 0, cut > 0, tiles * NT // 256 > 1
+
+
+def test_layouts_are_the_kernels(counts):
+    """The copy of the rule by which the layouts' coverage is asserted gives what the kernel
+    does, for the shapes there and others."""
+    rng = random.Random(1)
+    for groups, n, _ in tiles.LAYOUTS:
+        for tn in (128, 192, 256):
+            NT = -(-n // tn)
+            assert row_layout(counts, groups, NT) == coverage.layout(groups, NT)
+    for _ in range(3000):
+        groups = [rng.choice([0, rng.randrange(700), 256 * rng.randrange(9), 256 * rng.randrange(9) + 3])
+                  for _ in range(rng.randrange(1, 30))]
+        NT = rng.randrange(1, 33)
+        if any(groups):
+            assert row_layout(counts, groups, NT) == coverage.layout(groups, NT), (groups, NT)
+
+
+def test_every_tile_of_a_group_once(counts):
+    out = (ctypes.c_uint * 2)()
+    for k in (1, 2, 5, 6, 7, 11, 12, 13, 18, 19, 64, 100):
+        for NT in (1, 3, 16):
+            got = []
+            for v in range(k * NT):
+                counts.band(v, k, NT, out)
+                got.append(tuple(out))
+            assert sorted(got) == [(r, c) for r in range(k) for c in range(NT)]
 
 
 def workgroups(tile, splits, T, N, E=1):
