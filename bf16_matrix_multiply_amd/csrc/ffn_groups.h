@@ -169,7 +169,8 @@ struct Groups {
     return t;
   }
   // The group of row tile r, with its number among the group's; of the full ones, of the
-  // small ones, or of both in the groups' order, the small one last.
+  // small ones, or of both in the groups' order, the small one last. (find: also of the
+  // tail's, after the groups'.)
   template <int TM>
   __device__ __forceinline__ Group find(const Tiles<TM>& t, int r) const {
     if (r >= t.grouped) return behind(t, r - t.grouped);
@@ -177,22 +178,20 @@ struct Groups {
   }
   template <int TM>
   __device__ __forceinline__ Group find_small(const Tiles<TM>& t, int r) const {
-    if (r >= t.grouped_small) return behind(t, 0);
     return search(r, t.first_small, t.own_small, [](int n) { return small_tiles<TM>(n); });
   }
   template <int TM>
   __device__ __forceinline__ Group find_any(const Tiles<TM>& t, int r) const {
-    const int grouped = t.grouped + t.grouped_small;
-    if (r >= grouped) return behind(t, r - grouped);
     return search(r, t.first + t.first_small, t.own + t.own_small,
                   [](int n) { return full_tiles<TM>(n) + small_tiles<TM>(n); });
   }
-
- private:
+  // The rows behind the last group.
   template <int TM>
   __device__ __forceinline__ Group behind(const Tiles<TM>& t, int tile) const {
     return {E, t.end_all, T - t.end_all, tile};
   }
+
+ private:
   // The group of item r, of which each group has items(rows) and this lane's `own` from
   // `first` on, and the item's number in the group.
   template <class Fn>
