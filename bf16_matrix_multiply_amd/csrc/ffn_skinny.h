@@ -11,11 +11,12 @@
 // same result on every run.
 //
 // Measured on MI355X, weights cold: one token through 2 x 8192 x 4096 bf16 22.4 us =
-// 6.0 TB/s, through 16384 x 16384 4-bit weights 23.7 us = 6.0 TB/s; a long read
-// reaches 6.5. Eight steps at a time, 16 waves, a second set of registers for the
-// next round, or loads that stay in the caches changed it by -1 to +4 us. 8-bit weights:
-// 16384 x 16384 43 us = 6.2 TB/s. By groups: 64 rows of 8 groups gated 4096 -> 8192 bf16
-// 156 us = 6.9 TB/s, 14 rows of 7 with 8-bit weights 76 us = 6.2 TB/s.
+// 6.0 TB/s, through 16384 x 16384 4-bit weights 23.7 us = 6.0 TB/s; a long read (1
+// GiB and more) reaches 7.1. Eight steps at a time, 16 waves, a second set of
+// registers for the next round, or loads that stay in the caches changed it by -1 to
+// +4 us. 8-bit weights: 16384 x 16384 43 us = 6.2 TB/s. By groups: 64 rows of 8
+// groups gated 4096 -> 8192 bf16 156-162 us = 6.6-6.9 TB/s, 14 rows of 7 with 8-bit
+// weights 76 us = 6.2 TB/s.
 //
 // Fragments as in ffn_tile.h: lane l supplies row l % 16 and the 16 bytes of
 // summed chunk l / 16, and holds D[m = l % 16][n = 4 (l / 16) .. + 3]. Loads go

@@ -67,13 +67,15 @@
 // for each wave with its reads and loads shifted, one barrier for two slabs, and
 // for 4 bits 32 x 32 x 64 MFMAs.
 //
-// By groups: 16384 rows of 8 groups, 8192 -> 4096 bf16, 855-875 us (as many operations as
-// the product of 8192^3; MFMA utilisation 0.66 at 1.5-1.6 GHz); weight gradients of 16384
-// rows of 16 groups, 2048 -> 4096 gated, 535-580 us (0.47 at 2.0 GHz: results of 537 MB
-// from sums of 32 slabs); 24576 rows of 64 groups, 2048 -> 1408 gated with projections kept,
-// f16, 350 us (0.44 at 1.9 GHz: each group's weight comes from memory for the few tiles
-// that share it; with one weight for all of them 296). 8192^3 with 8-bit integers 375-385 us
-// = 2.9 PTOP/s (0.70 at 1.9 GHz).
+// By groups: 16384 rows of 8 groups, 8192 -> 4096 bf16, 847-895 us (as many operations
+// as the product of 8192^3; MFMA utilisation 0.66 at 1.5-1.6 GHz), of which a last
+// round of a few small tiles, with the whole sum each, takes 67 (groups of whole tiles:
+// 826); dX of 16384 rows of 16 groups, 2048 -> 4096 gated, 500-527 us, of which that
+// round 85 (440); its weight gradients 535-580 us (0.47 at 2.0 GHz: results of 537 MB
+// from sums of 32 slabs); 24576 rows of 64 groups, 2048 -> 1408 gated with projections
+// kept, f16, 350 us (0.44 at 1.9 GHz: each group's weight comes from memory for the few
+// tiles that share it; with one weight for all of them 296). 8192^3 with 8-bit integers
+// 375-385 us = 2.9 PTOP/s (0.70 at 1.9 GHz).
 // What writes the results faster in a probe, four lanes side by side on 64 bytes of a row,
 // did not pay by groups: with the lanes' results turned in registers for it, the weight
 // gradients of 24576 rows of 64 groups, 2048 x 1408, took 213 us instead of 219, those with
@@ -530,7 +532,8 @@ __device__ __forceinline__ bool locate_rows(const TileArgs& p, uint32_t w, uint3
   const Group g = tail ? groups.behind(rows, r)
                   : lasts ? groups.find_small<TM>(rows, r)
                   : mixed ? groups.find_any<TM>(rows, r) : groups.find<TM>(rows, r);
-  const int k = tail ? int(MT) : lasts ? 1 : full_tiles<TM>(g.rows) + (mixed ? small_tiles<TM>(g.rows) : 0);
+  const int k = tail ? int(MT) : lasts ? 1
+                : full_tiles<TM>(g.rows) + (mixed ? small_tiles<TM>(g.rows) : 0);
   const BandTile t = band_tile(w - uint32_t(r - g.tile) * NT, uint32_t(k), NT);
   at.empty = tail;
   at.b = tail ? 0 : g.e;

@@ -210,23 +210,26 @@ hipError_t launch_grouped_dw(const TileArgs& a, int dtype, hipStream_t s) {
 }
 
 // The plan that a simple model finds fastest. A tile of each size takes so many
-// nanoseconds a slab and so many besides (its first loads and its results) on a
-// full chip (256 workgroups; 128 x 128: 512). The tiles run in rounds; one that
-// fills a share f of the chip takes a + (1 - a) f of a full one, with another a for
-// the first round than for a later one, which starts while the one before it ends.
-// Split sums are written and read once, 8 bytes at 5 TB/s, and joined by one more
-// launch. The constants are a fit to 60 products measured on MI355X (16-bit and
-// 4-bit, 200 to 32773 rows): 7% off in the mean, and within 3% of the fastest size
-// in all but two. For example gated K = 2048 -> 5464 by tiles of 128 x 128, 256 x
-// 128, 256 x 192 and 256 x 256: 777 rows 45.5, 52.3, 39.0 and 43.2 us, 1500 rows
-// 70, 83, 77 and 92, 4095 rows 163, 172, 164 and 148; the weight gradients of 32773
-// x 512 -> 1024 by 128 x 128 tiles 258 us, by 256 x 128 tiles and 8 splits 72.
-// Outside of those products it is rougher. Below 128 rows it expects too little (96
-// x 4096 -> 8192: 38 us, measured 45), without a worse choice. It does not know that a
-// gated call keeps its projections: where the sum is short, 128 x 128 tiles are then
-// often the better ones (kept, 4096 x 256 -> 4096: 47 us, chosen 256 x 256 56; 16384 x
-// 256 -> 2048: 83, chosen 97; but 8192 x 256 -> 8192: 230, chosen 159), and 256 x 192
-// tiles, which write the last columns in pieces of 32 bytes, the slowest (369 there).
+// nanoseconds a slab and so many besides (its first loads and its results) on a full
+// chip (256 workgroups; 128 x 128: 512). The tiles run in rounds; one that fills a
+// share f of the chip takes a + (1 - a) f of a full one, with another a for the first
+// round than for a later one, which starts while the one before it ends. Split sums are
+// written and read once, 8 bytes at 5 TB/s, and joined by one more launch. The
+// constants are a fit to 60 products measured on MI355X (16-bit and 4-bit, 200 to 32773
+// rows): 7% off in the mean, and within 3% of the fastest size in all but two. For
+// example gated K = 2048 -> 5464 by tiles of 128 x 128, 256 x 128, 256 x 192 and 256 x
+// 256: 777 rows 45.5, 52.3, 39.0 and 43.2 us, 1500 rows 70, 83, 77 and 92, 4095 rows
+// 163, 172, 164 and 148; the weight gradients of 32773 x 512 -> 1024 by 128 x 128 tiles
+// 258 us, by 256 x 128 tiles and 8 splits 72. Of 98 products and gated blocks of 8-bit
+// integers (80 to 8192 rows, 1024 -> 4096 to 14336 -> 4096), which it does not tell
+// from 16-bit ones of as many slabs, it takes a size within 3% of the fastest in 94, at
+// worst 10% off. Outside of those products it is rougher. Below 128 rows it expects too
+// little (96 x 4096 -> 8192: 38 us, measured 45), without a worse choice. It does not
+// know that a gated call keeps its projections: where the sum is short, 128 x 128 tiles
+// are then often the better ones (kept, 4096 x 256 -> 4096: 47 us, chosen 256 x 256 56;
+// 16384 x 256 -> 2048: 83, chosen 97; but 8192 x 256 -> 8192: 230, chosen 159), and 256
+// x 192 tiles, which write the last columns in pieces of 32 bytes, the slowest (369
+// there).
 namespace {
 
 // row_tiles(tm): tiles of tm rows; most(tm): as many at most; outputs: values that a split
@@ -275,7 +278,10 @@ TilePlan plan_tiles(int64_t batch, int64_t M, int64_t N, int64_t slabs, bool may
 }
 
 // The host knows T rows and E groups, not how the rows fall on them: groups that have
-// rows have n in the mean, and the last tile of one is half full.
+// rows have n in the mean, and the last tile of one is half full. Of 78 8-bit products and
+// gated blocks by groups that differ by half in size (400 rows of 8 to 24576 of 64) the size
+// is within 3% of the fastest in 62 and 2.8% off in the mean; worst where few columns make
+// few tiles: 16384 rows of 4 groups, 4320 -> 416, by 128 x 128 tiles 57 us, by 256 x 192 42.
 TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool may_split) {
   const double some = double(E < T ? E : T), n = some > 0 ? T / some : 0;
   auto row_tiles = [&](int64_t tm) {
@@ -289,7 +295,10 @@ TilePlan plan_group_rows(int64_t E, int64_t T, int64_t N, int64_t slabs, bool ma
 // Sums over the rows of E groups of T. Their many results make the difference between the
 // sizes: 24576 rows of 64 groups, 2048 x 1408, by tiles of 128 x 128, 256 x 128, 256 x 192
 // and 256 x 256: 252, 251, 232 and 211 us; 16384 rows of 16 groups, 8192 x 2048: 694, 643,
-// 559 and 529 us.
+// 559 and 529 us. Of 55 sums (1 to 128 groups, 2000 to 32768 rows, 512 x 1024 to 4096 x 4096)
+// the plan is within 3% of the fastest size in 40 and 2.9% off in the mean; worst 8192 rows
+// of 32 groups, 2048 x 2048, by 256 x 256 tiles 144 us, by 256 x 192 118, and 512 x 1024 27,
+// by 128 x 128 22.
 TilePlan plan_group_sums(int64_t E, int64_t T, int64_t M, int64_t N, bool small) {
   static constexpr double kExtra[4] = {2300, 1100, 500, 700};
   auto row_tiles = [&](int64_t tm) { return double(E) * ((M + tm - 1) / tm); };
@@ -326,9 +335,22 @@ int plan_forward(int64_t batch, int64_t M, int64_t N, int64_t slabs) {
 //   512 tiles: 8 x 4096 -> 8192       87.0/93.4   101/92.3    113/93.3    172/97.5    325/123
 //   1024 tiles: 64 x 1408 -> 2048     62.4/66.3   80.2/67.9   91.7/69.9   131/78.1    219/89.1
 // and with 8-bit operands alike (8 x 4096 -> 8192: 43.2/48.6, 52.8/47.9, 56.1/48.9). The
-// groups there differ by half in size; more alike ones suit the few-rows kernel (64 rows
-// and a tail of 16 of 8 groups gated 4096 -> 8192: 156 us in its blocks of 16, 208 in
-// tiles), so that up to 10 rows are its own everywhere.
+// groups there differ by half in size, and one with more than 16 rows reads its weight
+// twice. Where tiles fill the chip, the few-rows kernel's time over the best tiles' with
+// such groups and with equal ones:
+//   rows a group                      7          8          10         11         14
+//   512 tiles: 8 x 4096 -> 8192       0.85/0.86  0.96/0.86  0.97/0.87  1.08/0.88  1.09/0.92
+//   512 tiles: 16 x 2048 -> 4096      0.90/0.89  0.93/0.88  1.03/0.89  0.95/0.89  1.13/0.92
+//   1024 tiles: 8 gated 4096 -> 8192  0.92/0.92  1.03/0.92  1.02/0.91  1.13/0.91  1.13/0.92
+//   1024 tiles: 64 x 1408 -> 2048     0.86/0.85  0.88/0.85  0.96/0.87  0.99/0.91  1.14/0.98
+//   1408 tiles: 64 gated 2048 -> 1408 0.94/0.96  0.99/0.97  1.05/0.97  1.06/0.98  1.16/0.97
+//   8 bits, 8 x 4096 -> 8192          0.86/0.87  0.95/0.85  0.96/0.87  1.04/0.87  1.04/0.89
+//   8 bits, 8 gated 4096 -> 8192      0.93/0.94  1.04/0.93  1.04/0.94  1.13/0.94  1.14/0.95
+// With different groups the two are even at 8 to 11 rows, with equal ones the few-rows
+// kernel stays ahead: up to 10 rows are its own everywhere, which costs at most 5%, and
+// beyond them equal groups pay up to 15%. Rows behind the last group count among a
+// group's (the host cannot tell them): 64 rows of 8 groups gated 4096 -> 8192 take 158 us
+// with a tail of 16 and 183 with one of 24.
 int plan_group_forward(int64_t E, int64_t T, int64_t N, int64_t slabs) {
   const int64_t some = E < T ? E : T, tiles = some * ((N + 127) / 128);
   if (tiles > 0) {

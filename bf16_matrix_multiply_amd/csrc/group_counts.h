@@ -78,7 +78,11 @@ constexpr RowLayout row_layout(uint32_t full, uint32_t small, uint32_t NT, uint3
 
 // Tile v of the k x NT tiles of one group, whose rows are taken in bands of 6 at most
 // and as equal as can be, so that the tiles of a band that run together share the
-// group's weight: its row and column.
+// group's weight: its row and column. Bands of at most 2, 4, 6, 8 and any number (us):
+// 16384 rows of 8 groups 8192 -> 4096 917, 889, 888, 883, 887; gated 4096 -> 4096 911, 879,
+// 870, 862, 864; of one group 4096 -> 4096 401, 379, 381, 380, 408; 32768 rows of 16, 4096
+// -> 1024 245, 246, 250, 251, 251; 24576 of 64 the same with each. From 4 to 8 it matters
+// little.
 struct BandTile {
   uint32_t row, col;
 };
