@@ -132,7 +132,7 @@ int bmm_gated_backward(uint16_t* dX, uint16_t* dWg, uint16_t* dWu, const uint16_
       peaks = reinterpret_cast<uint32_t*>(rescale + 1);
     }
     int rc = bmm::hip_status(bmm::launch_gated_slopes(dgu, dH, G, U, d.batch * d.M, d.F, d.ld_h,
-                                                 d.dtype, d.act, nullptr, peaks, rescale, s),
+                                                 d.dtype, d.act, {}, peaks, rescale, s),
                         "gated_backward slopes launch");
     if (rc != BMM_OK) return rc;
     auto rows_of_dx = [&](int64_t row, int64_t rows, const bmm::TilePlan& tiles) {

@@ -121,7 +121,7 @@ int grouped_backward(const bmm::GroupedGrads& g, const int32_t* ends, const bmm_
     }
     const int rc = hip_status(
         bmm::launch_gated_slopes(dgu, g.dY, g.G, g.U, d.T, d.N, d.ld_y, d.dtype, d.act,
-                                 ends + d.groups - 1, peaks, rescale, s),
+                                 {ends, int(d.groups), int(d.T)}, peaks, rescale, s),
         "grouped_gated_backward slopes launch");
     if (rc != BMM_OK) return rc;
     dy = dgu;

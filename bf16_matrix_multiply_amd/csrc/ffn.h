@@ -69,6 +69,12 @@ struct TileArgs {
   const float* sb1;
 };
 
+// Where the groups of so many rows end; without groups (null) all rows count.
+struct GroupEnds {
+  const int32_t* at = nullptr;
+  int groups = 0, rows = 0;
+};
+
 // ---- launchers ----
 hipError_t launch_gated(const TileArgs& a, int dtype, hipStream_t s);
 // dG = dH U act'(G), dU = dH act(G), rounded to the operands' type, as (rows, 2 Fp) row-major
@@ -78,8 +84,8 @@ hipError_t launch_gated(const TileArgs& a, int dtype, hipStream_t s);
 int64_t gated_peaks(int64_t rows, int64_t F);
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, const int32_t* end, uint32_t* peaks, float* rescale,
-                               hipStream_t s);   // end: rows from *end on are not made (null: all)
+                               int act, GroupEnds ends, uint32_t* peaks, float* rescale,
+                               hipStream_t s);   // (rows behind the groups' are not made)
 hipError_t launch_gated_dx(const TileArgs& a, int dtype, hipStream_t s);
 hipError_t launch_gated_dw(const TileArgs& a, int dtype, hipStream_t s);
 // By groups of rows (ffn_groups.h).

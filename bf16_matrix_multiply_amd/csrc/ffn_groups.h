@@ -36,6 +36,15 @@ __device__ __forceinline__ int lanes_max(int x) {
 __device__ __forceinline__ int lanes_sum(int x) {
   return lanes_scan(x, 0, [](int a, int b) { return a + b; });
 }
+// The rows of E groups in all, as Groups holds their ends, in every lane.
+__device__ __forceinline__ int rows_of_groups(const int32_t* ends, int E, int T, int lane) {
+  int top = 0;
+  for (int e = lane; e < E; e += kWave) {
+    const int x = ends[e] < T ? ends[e] : T;
+    top = x > top ? x : top;
+  }
+  return __builtin_amdgcn_readlane(lanes_max(top), kWave - 1);
+}
 // The value of the lane before; lane 0: 0.
 __device__ __forceinline__ int lane_before(int x) {
   return __builtin_amdgcn_update_dpp(0, x, 0x138, 0xf, 0xf, false);   // wave_shr:1

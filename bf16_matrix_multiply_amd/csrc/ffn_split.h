@@ -16,13 +16,16 @@ constexpr int kJoinThreads = 256;
 template <int DT, int GRP>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(TileArgs p, int64_t n8) {
   const int64_t stride = int64_t(gridDim.x) * kJoinThreads;
+  int64_t rows = p.M;   // that have a result
+  if (GRP == kGroupRows && !p.zero_tail)
+    rows = rows_of_groups(p.ends, int(p.batch), int(p.M), threadIdx.x % kWave);
   for (int64_t i = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x; i < n8; i += stride) {
     const int64_t row = 8 * i / p.N, col = 8 * i % p.N;
     const int64_t b = row / p.M, m = row % p.M;
     const bool second = m >= p.row1;
     const int64_t r = second ? m - p.row1 : m;
     if (r >= p.rows0) continue;
-    if (GRP == kGroupRows && !p.zero_tail && (p.batch == 0 || m >= p.ends[p.batch - 1])) continue;
+    if (GRP == kGroupRows && m >= rows) continue;
     f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
     for (int s = 0; s < p.splits; ++s) {
       const float* at = p.part + s * p.part_floats + 8 * i;

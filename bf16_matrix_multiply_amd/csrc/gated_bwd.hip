@@ -57,12 +57,11 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x) {
   return x;
 }
 
-// n items, per_row a row, held to the rows before *end (groups: what lies behind the
-// last one is not read).
-__device__ __forceinline__ int64_t rows_until(const int32_t* end, int64_t n, int64_t per_row) {
-  if (!end) return n;
-  const int64_t rows = *end, m = rows > 0 ? rows * per_row : 0;
-  return m < n ? m : n;
+// n items, per_row a row, of which those of the groups' rows count (what lies behind the
+// last group is not read). Every lane of the wave takes part.
+__device__ __forceinline__ int64_t rows_until(GroupEnds ends, int64_t n, int64_t per_row) {
+  if (!ends.at) return n;
+  return ffn::rows_of_groups(ends.at, ends.groups, ends.rows, threadIdx.x % kWave) * per_row;
 }
 
 // The largest finite magnitude of dG and dU that each workgroup meets, as float32
@@ -75,10 +74,10 @@ __global__ __launch_bounds__(kThreads) void peaks_kernel(uint32_t* __restrict__ 
                                                          const uint16_t* __restrict__ g,
                                                          const uint16_t* __restrict__ u, int64_t n,
                                                          int64_t F, int64_t ld,
-                                                         const int32_t* __restrict__ end) {
+                                                         GroupEnds ends) {
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t per_row = F / 8;
-  n = rows_until(end, n, per_row);
+  n = rows_until(ends, n, per_row);
   uint32_t top = 0;
   for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += stride) {
     const int64_t row = i / per_row, f = 8 * (i % per_row);
@@ -103,13 +102,13 @@ __global__ __launch_bounds__(kThreads) void slopes_kernel(uint16_t* __restrict__
                                                           const uint16_t* __restrict__ u,
                                                           int64_t n, int64_t F, int64_t Fp,
                                                           int64_t ld,
-                                                          const int32_t* __restrict__ end,
+                                                          GroupEnds ends,
                                                           const uint32_t* __restrict__ peaks,
                                                           int n_peaks,
                                                           float* __restrict__ rescale) {
   const int64_t stride = int64_t(gridDim.x) * kThreads;
   const int64_t per_row = Fp / 8;
-  n = rows_until(end, n, per_row);
+  n = rows_until(ends, n, per_row);
   float scale = 1.f;
   if constexpr (DT == kF16) {
     uint32_t top = 0;
@@ -157,7 +156,7 @@ int64_t gated_peaks(int64_t rows, int64_t F) {
 
 hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t* g,
                                const uint16_t* u, int64_t rows, int64_t F, int64_t ld, int dtype,
-                               int act, const int32_t* end, uint32_t* peaks, float* rescale,
+                               int act, GroupEnds ends, uint32_t* peaks, float* rescale,
                                hipStream_t s) {
   const int64_t Fp = (F + 31) / 32 * 32, n = rows * Fp / 8;
   if (n == 0) return hipSuccess;
@@ -173,13 +172,13 @@ hipError_t launch_gated_slopes(uint16_t* dgu, const uint16_t* dh, const uint16_t
   if (dtype == kF16) {
     hipLaunchKernelGGL(by_act([](auto a) { return peaks_kernel<kF16, decltype(a)::value>; }),
                        dim3(unsigned(n_peaks)), dim3(kThreads), 0, s, peaks, dh, g, u, rows * F / 8,
-                       F, ld, end);
+                       F, ld, ends);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   auto kern = dtype == kBF16 ? by_act([](auto a) { return slopes_kernel<kBF16, decltype(a)::value>; })
                              : by_act([](auto a) { return slopes_kernel<kF16, decltype(a)::value>; });
-  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld, end,
+  hipLaunchKernelGGL(kern, dim3(grid_for(n)), dim3(kThreads), 0, s, dgu, dh, g, u, n, F, Fp, ld, ends,
                      peaks, n_peaks, rescale);
   return hipGetLastError();
 }

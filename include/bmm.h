@@ -602,8 +602,8 @@ int bmm_ffn_plan(int32_t product, int64_t batch, int64_t M, int64_t F, int64_t K
  * they are not read, and their outputs become zero with zero_tail and stay as
  * they are without. ends is device memory and is read by the kernels only, so a
  * captured graph takes other groups on every replay. Ends are held to 0 .. T and
- * to be no smaller than the ones before: other values give meaningless outputs,
- * but nothing outside of the matrices is touched.
+ * to be no smaller than the ones before: other values count as the nearest such
+ * ones, and nothing outside of the matrices is touched.
  *
  * Extents of a product by groups.
  *   groups     1 .. 4096
