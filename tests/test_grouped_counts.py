@@ -2,6 +2,7 @@
 kernels use) against Python's whole numbers, up to 2^31 - 1 rows (CPU); and products of
 that many rows on the GPU, which one launch of fewer than 2^32 threads has to hold."""
 import ctypes
+import gc
 import os
 import random
 import subprocess
@@ -168,8 +169,16 @@ def test_more_tiles_than_a_launch_holds(L):  # noqa: F811
     assert "more tiles than one launch may have" in err(L)
 
 
+@pytest.fixture
+def much_memory():
+    """Up to 160 GiB, given back at the end."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.gpu
-def test_weight_gradient_of_the_most_rows():
+def test_weight_gradient_of_the_most_rows(much_memory):
     """2^31 - 1 rows in one group, and in three; all of them zeros but a few at the ends of
     the groups and of the sums' parts."""
     K, N = 16, 8
@@ -191,7 +200,7 @@ def test_weight_gradient_of_the_most_rows():
 
 
 @pytest.mark.gpu
-def test_products_of_the_most_rows():
+def test_products_of_the_most_rows(much_memory):
     """Forward product and dX of 2^31 - 1 rows, zeros but for a few; every output written."""
     K, N = 16, 8
     at = torch.tensor([0, 255, 256, 5000, TOP // 2, TOP - 257, TOP - 256, TOP - 1], device="cuda")
